@@ -60,9 +60,19 @@ typedef enum {
 
 typedef enum {
     SSD_F32 = 0,   /* x, Bm, Cm, y in fp32: SIMT fp32 path (|rel err| ~1e-6) */
-    SSD_BF16 = 1   /* x, Bm, Cm, y in bf16, fp32 accumulate: tensor-core path for the
+    SSD_BF16 = 1,  /* x, Bm, Cm, y in bf16, fp32 accumulate: tensor-core path for the
                       sizes ssd_forward lists, SIMT path otherwise */
+    SSD_E4M3 = 2   /* 8-bit values (one sign, four exponent, three mantissa bits) with
+                      fp32 scales beside them: ssd_rms_norm's output, ssd_linear's
+                      operands. Not an I/O dtype of the SSD core. */
 } ssd_dtype;
+
+/* Activation of ssd_linear and of ssd_conv (which has no GELU). */
+typedef enum {
+    SSD_ACT_NONE = 0,
+    SSD_ACT_SILU = 1,  /* v / (1 + exp(-v)) */
+    SSD_ACT_GELU = 2   /* v (1 + erf(v / sqrt 2)) / 2 */
+} ssd_activation;
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* ssd_status_string(ssd_status status);
@@ -185,6 +195,106 @@ ssd_status ssd_forward_host(const void* x_host, const float* dt_host, const floa
 ssd_status ssd_step(const void* x, const float* dt, const float* A, const void* Bm,
                     const void* Cm, const float* D, float* state, void* y, int B, int H,
                     int P, int G, int N, ssd_dtype dtype, ssd_stream_t stream);
+
+/*
+ * The operators around the SSD core of a Mamba-2 layer ("Mamba-2", section
+ * "Mamba-2 block": one in-projection for the gate, x, B, C and the step sizes,
+ * a short convolution, the SSD core, gate and norm, the out-projection). They
+ * follow the conventions at the top; strides count elements, and a strided
+ * operand's last dimension is contiguous. Outputs must not overlap inputs or
+ * each other except where an entry says so. Sums and statistics are fp32;
+ * an output is rounded once, to nearest even. No entry here waits on the
+ * device or needs a workspace but where it says so, so calls on different
+ * streams may overlap freely.
+ */
+
+/*
+ * ssd_rms_norm — root-mean-square norm over rows, after the residual's
+ * addition (the norm before a block) or the gate (the norm after the SSD
+ * core), to the I/O dtype or to 8 bits with one scale per row:
+ *     v = x + residual   or   v = x * silu(gate)   or   v = x
+ *     y_j = v_j * weight_j / sqrt(mean(v^2 over j's group) + eps)
+ *     8 bits: scale = max(max_j |y_j| / 448, 2^-126), y_j stored as
+ *     e4m3(y_j / scale), so y_j ~ scale * stored
+ *   x         [rows, D]   I/O dtype (`dtype`)
+ *   residual  [rows, D]   `residual_dtype` (fp32 or `dtype`); NULL: none
+ *   gate      row r at gate + r * gate_stride, I/O dtype; NULL: none. Not
+ *             together with residual. Any alignment (16-byte rows are faster).
+ *   weight    [D]         fp32
+ *   y         [rows, D]   `y_dtype`: `dtype`, or SSD_E4M3 with scale
+ *   scale     [rows]      fp32; with SSD_E4M3 and only then
+ *   residual_out [rows, D] `residual_dtype`: v rounded (the norm itself reads
+ *             v before this rounding); NULL to skip. May be residual itself.
+ *   y may be x itself when y_dtype == dtype.
+ *   A row that holds a NaN, or whose sum of squares overflows fp32, has NaN
+ *   or zero outputs as the formulas in fp32 give them.
+ *   Sizes: rows >= 0 (0 is a no-op), D in [1, 2^20], groups in [1, 32]
+ *   dividing D.
+ */
+ssd_status ssd_rms_norm(const void* x, const void* residual, const void* gate, int64_t gate_stride,
+                        const float* weight, void* y, float* scale, void* residual_out,
+                        int64_t rows, int D, int groups, float eps, ssd_dtype dtype,
+                        ssd_dtype residual_dtype, ssd_dtype y_dtype, ssd_stream_t stream);
+
+/*
+ * ssd_linear — matrix product with its epilogue (the in- and out-projection):
+ *     y[m, n] = act(x_scale[m] * w_scale[n] * sum_k x[m, k] w[n, k] + bias[n])
+ *               + residual[m, n]
+ *   x         row m at x + m * x_stride, K elements, `dtype`
+ *   w         [N, K]      `dtype`
+ *   x_scale   [M], w_scale [N]  fp32; with SSD_E4M3 operands and only then
+ *   bias      [N]         fp32 or NULL
+ *   residual  [M, N]      `y_dtype` or NULL. May be y itself.
+ *   y         [M, N]      `y_dtype`: SSD_F32 or SSD_BF16
+ *   dtype     SSD_F32, SSD_BF16 or SSD_E4M3, of both operands
+ *   Sizes: M, N >= 0 (0 is a no-op), K >= 1; N, K <= 2^20. x needs its
+ *   element's alignment only; every other pointer is 16-byte aligned.
+ */
+ssd_status ssd_linear(const void* x, int64_t x_stride, const void* w, const float* x_scale,
+                      const float* w_scale, const float* bias, const void* residual, void* y, int M,
+                      int N, int K, ssd_activation act, ssd_dtype dtype, ssd_dtype y_dtype,
+                      ssd_stream_t stream);
+
+/*
+ * ssd_conv — short causal convolution of every channel, and the cut of the
+ * in-projection's rows into ssd_forward's operands:
+ *     v[t, c] = bias[c] + sum_k weight[c, k] * u[t - width + 1 + k, c]
+ *     [x | Bm | Cm][t] = act(v[t]);  dt[t, h] = log(1 + exp(dt_raw[t, h] + dt_bias[h]))
+ *   u         token t of batch row b at u + b * u_batch_stride + t * u_row_stride:
+ *             C = H P + 2 G N channels, I/O dtype, any alignment (16-byte
+ *             rows are faster)
+ *   weight    [C, width]  fp32; weight[c, width - 1] multiplies the token itself
+ *   bias      [C]         fp32 or NULL
+ *   dt_raw    H step sizes per token, strided like u, I/O dtype; NULL: dt is
+ *             not written and must be NULL
+ *   dt_bias   [H]         fp32 or NULL
+ *   initial_state [B, width - 1, C] I/O dtype: the inputs before token 0, the
+ *             oldest first; NULL means zeros
+ *   x [B, L, H, P], Bm, Cm [B, L, G, N] I/O dtype; dt [B, L, H] fp32
+ *   final_state [B, width - 1, C] I/O dtype: the last width - 1 inputs (of the
+ *             state and u in a row, when L < width - 1); NULL to skip. Must not
+ *             overlap initial_state.
+ *   act       SSD_ACT_NONE or SSD_ACT_SILU
+ *   Sizes: as ssd_forward for B, L, H, P, G, N (B*L == 0 is a no-op apart from
+ *   final_state = initial_state or 0); B <= 65535; width in 2..4.
+ */
+ssd_status ssd_conv(const void* u, int64_t u_batch_stride, int64_t u_row_stride, const float* weight,
+                    const float* bias, const void* dt_raw, int64_t dt_batch_stride,
+                    int64_t dt_row_stride, const float* dt_bias, const void* initial_state, void* x,
+                    void* Bm, void* Cm, float* dt, void* final_state, int B, int L, int H, int P,
+                    int G, int N, int width, ssd_activation act, ssd_dtype dtype,
+                    ssd_stream_t stream);
+
+/*
+ * ssd_conv_step — the same for one token per sequence, before ssd_step:
+ * u [B, C] with row stride u_stride, dt_raw [B, H] with row stride dt_stride,
+ * state [B, width - 1, C] I/O dtype, shifted in place; x [B, H, P],
+ * Bm, Cm [B, G, N], dt [B, H].
+ */
+ssd_status ssd_conv_step(const void* u, int64_t u_stride, const float* weight, const float* bias,
+                         const void* dt_raw, int64_t dt_stride, const float* dt_bias, void* state,
+                         void* x, void* Bm, void* Cm, float* dt, int B, int H, int P, int G, int N,
+                         int width, ssd_activation act, ssd_dtype dtype, ssd_stream_t stream);
 
 /* Number of kernels one ssd_forward call with these sizes enqueues (0 if the
  * sizes are invalid or there are no tokens): 1 for the tensor-core single

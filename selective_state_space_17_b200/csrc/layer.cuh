@@ -1,0 +1,157 @@
+// layer.cuh — arguments and launchers of the operators around the SSD core
+// (norm.cu, conv.cu, linear.cu) as layer_api.cu calls them, and the device
+// helpers they share.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+
+namespace ssd {
+
+// Root-mean-square norm (norm.cu). Exactly one of residual and gate may be set.
+struct NormArgs {
+    const void* x;          // [rows, D], I/O dtype
+    const void* residual;   // [rows, D] in res_f32 ? fp32 : I/O dtype, or null
+    const void* gate;       // row r at gate + r * gate_stride, I/O dtype, or null
+    long long gate_stride;  // elements
+    const float* weight;    // [D]
+    void* y;                // [rows, D], e4m3 when scale is set, else the I/O dtype
+    float* scale;           // [rows], or null
+    void* residual_out;     // as residual, or null
+    long long rows;
+    int D, groups;
+    float eps;
+    bool bf16, res_f32;
+};
+cudaError_t rms_norm(const NormArgs& a, const LaunchCtx& ctx);
+
+// Short causal convolution (conv.cu).
+struct ConvArgs {
+    const void* u;           // token t of row b at u + b * u_batch + t * u_row
+    long long u_batch, u_row;
+    const float* weight;     // [C, W]
+    const float* bias;       // [C] or null
+    const void* dt_raw;      // [.., H] beside u, or null
+    long long dt_batch, dt_row;
+    const float* dt_bias;    // [H] or null
+    const void* init;        // [B, W-1, C] or null (zeros)
+    void* x;                 // [B, L, XC]
+    void* Bm;                // [B, L, GN]
+    void* Cm;                // [B, L, GN]
+    float* dt;               // [B, L, H]
+    void* final_state;       // [B, W-1, C] or null; may be init when L == 1
+    int B, L, H, XC, GN, W;
+    bool silu, bf16;
+    __host__ __device__ int C() const { return XC + 2 * GN; }
+};
+cudaError_t conv_forward(const ConvArgs& a, const LaunchCtx& ctx);
+
+// Matrix product with its epilogue (linear.cu, linear_simt.cu).
+enum class LinearType { f32, bf16, e4m3 };
+struct LinearArgs {
+    const void* x;         // row m at x + m * x_stride
+    long long x_stride;    // elements
+    const void* w;         // [N, K]
+    const float* x_scale;  // [M] or null
+    const float* w_scale;  // [N] or null
+    const float* bias;     // [N] or null
+    const void* residual;  // [M, N] in the output's dtype, or null
+    void* y;               // [M, N] fp32 or bf16
+    int M, N, K;
+    int act;               // ssd_activation
+    LinearType type;
+    bool out_bf16;
+};
+cudaError_t linear_simt(const LinearArgs& a, const LaunchCtx& ctx);
+
+inline bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+
+// v * sigmoid(v). exp of a large negative v's opposite is inf, which divides
+// to 0; the fast exponential and division are off by a few units of 2^-24,
+// below every output's rounding but fp32's, where the sum of both measured
+// 2e-7 of the output.
+__device__ __forceinline__ float silu_f(float v) { return __fdividef(v, 1.0f + __expf(-v)); }
+
+__device__ __forceinline__ float gelu_f(float v)
+{
+    // 0.5 v (1 + erf(v / sqrt 2)) as 0.5 v erfc(-v / sqrt 2), which keeps its
+    // relative precision where the sum would cancel (v << 0)
+    return 0.5f * v * erfcf(-0.70710678118654752f * v);
+}
+
+__device__ __forceinline__ float activate(float v, int act)
+{
+    if (act == SSD_ACT_SILU) return silu_f(v);
+    if (act == SSD_ACT_GELU) return gelu_f(v);
+    return v;
+}
+
+// VEC consecutive elements of type T as they lie in memory (one access of up
+// to 16 bytes each, two for 32 bytes), and as fp32 values.
+template <typename T, int VEC>
+struct Packed {
+    static constexpr int kBytes = VEC * (int)sizeof(T);
+    static constexpr int kWords = kBytes >= 4 ? kBytes / 4 : 1;
+    uint32_t w[kWords];
+
+    __device__ __forceinline__ void load(const T* p)
+    {
+        if constexpr (kBytes >= 16) {
+#pragma unroll
+            for (int i = 0; i < kBytes / 16; ++i) {
+                const uint4 v = *(reinterpret_cast<const uint4*>(p) + i);
+                w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+            }
+        } else if constexpr (kBytes == 8) {
+            const uint2 v = *reinterpret_cast<const uint2*>(p);
+            w[0] = v.x; w[1] = v.y;
+        } else if constexpr (kBytes == 4) {
+            w[0] = *reinterpret_cast<const uint32_t*>(p);
+        } else {
+            w[0] = *reinterpret_cast<const uint16_t*>(p);
+        }
+    }
+    __device__ __forceinline__ void store(T* p) const
+    {
+        if constexpr (kBytes >= 16) {
+#pragma unroll
+            for (int i = 0; i < kBytes / 16; ++i)
+                *(reinterpret_cast<uint4*>(p) + i) =
+                    make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        } else if constexpr (kBytes == 8) {
+            *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+        } else if constexpr (kBytes == 4) {
+            *reinterpret_cast<uint32_t*>(p) = w[0];
+        } else {
+            *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(w[0]);
+        }
+    }
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ float get(int i) const
+    {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else return __uint_as_float((i & 1) ? (w[i / 2] & 0xFFFF0000u) : (w[i / 2] << 16));
+    }
+    __device__ __forceinline__ void set(const float* v)
+    {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) w[i] = __float_as_uint(v[i]);
+        } else if constexpr (VEC == 1) {
+            w[0] = __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC / 2; ++i) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+        }
+    }
+};
+
+}  // namespace ssd
