@@ -63,7 +63,8 @@ struct LinearArgs {
     LinearType type;
     bool out_bf16;
 };
-cudaError_t linear_simt(const LinearArgs& a, const LaunchCtx& ctx);
+cudaError_t linear(const LinearArgs& a, const LaunchCtx& ctx);       // the tensor cores where they can
+cudaError_t linear_simt(const LinearArgs& a, const LaunchCtx& ctx);  // any operands
 
 inline bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 

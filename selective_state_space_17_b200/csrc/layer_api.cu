@@ -167,7 +167,7 @@ ssd_status ssd_linear(const void* x, int64_t x_stride, const void* w, const floa
     a.residual = residual; a.y = y; a.M = M; a.N = N; a.K = K; a.act = act;
     a.type = dtype == SSD_F32 ? LinearType::f32 : dtype == SSD_BF16 ? LinearType::bf16 : LinearType::e4m3;
     a.out_bf16 = y_dtype == SSD_BF16;
-    return launched(linear_simt(a, ctx));
+    return launched(linear(a, ctx));
 }
 
 ssd_status ssd_conv(const void* u, int64_t u_batch_stride, int64_t u_row_stride, const float* weight,

@@ -1,0 +1,300 @@
+// linear.cu — matrix product with its epilogue on the tensor cores (tcgen05),
+// bf16 or e4m3 operands:
+//
+//     y[m, n] = act(xs[m] ws[n] sum_k x[m, k] w[n, k] + bias[n]) + residual[m, n]
+//
+// Two kernels. Few tokens (linear_few_kernel): the weights' bytes bound the
+// call, so w takes the 128 lanes of the accumulator, the tokens its columns,
+// and the K axis is cut over a cluster of CTAs that join their parts through
+// distributed shared memory. Many tokens (linear_many_kernel): the tensor cores
+// bound the call; persistent CTA pairs on 256-row tiles.
+//
+// Both stage operand rows of 128 bytes (64 bf16 or 128 e4m3 values) by TMA with
+// the 128-byte swizzle; one tcgen05.mma takes 32 bytes of each row, whatever
+// the type, so the two types share all but the instruction.
+#include <algorithm>
+
+#include "layer.cuh"
+#include "sm100_mma.cuh"
+
+namespace ssd {
+namespace {
+
+using namespace sm100;
+
+constexpr int kRowBytes = 128;  // bytes of an operand row in one stage
+
+struct Epilogue {
+    const float* x_scale;
+    const float* w_scale;
+    const float* bias;
+    const void* residual;
+    void* y;
+    int M, N, act;
+};
+
+// ------------------------------------------------------------- few tokens
+
+// One CTA: 128 channels x BN tokens over its part of K. The parts of a cluster
+// meet in shared memory: every CTA writes its fp32 tile there, and CTA r adds up
+// the tokens r, r + S, ... in the order of the ranks, so the sum does not depend
+// on who is first. Within a CTA the K axis is cut again into segments with an
+// accumulator each: the tensor cores truncate each addition, a bias that grows
+// with the additions in a row (-4.7e-6 of the result after 5120 bf16 products,
+// -0.8e-6 after 1024), and the segments are joined with rounded additions.
+template <int BN>
+struct Few {
+    static constexpr int kStageBytes = 128 * kRowBytes + BN * kRowBytes;
+    // two CTAs per SM, whose loads in flight together cover HBM's latency
+    static constexpr int kStages = std::min(6, (110 * 1024) / kStageBytes);
+    static constexpr int kRedBytes = BN * 128 * 4;
+    static constexpr int kData = std::max(kStages * kStageBytes, kRedBytes);
+    static constexpr int kSmem = 1024 + kData + 256;
+    static constexpr int kMaxSegments = BN >= 128 ? 2 : 4;
+};
+
+template <int BN, bool E4M3, typename O>
+__global__ void __launch_bounds__(128)
+linear_few_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+                  const Epilogue e, int kblocks, int seg_blocks, uint32_t tmem_cols, unsigned int* status)
+{
+    using F = Few<BN>;
+    constexpr int NS = F::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(sm + F::kData);
+    uint64_t* empty = full + NS;
+    uint64_t* done = empty + NS;
+    uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(done + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_ptr + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int splits = gridDim.x;
+    const int rank = blockIdx.x;  // the cluster spans x: the rank within it
+    const int n0 = blockIdx.y * 128, m0 = blockIdx.z * BN;
+    const int kb0 = (int)((long long)kblocks * rank / splits);
+    const int kb1 = (int)((long long)kblocks * (rank + 1) / splits);
+    const int count = kb1 - kb0;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, 1);
+        }
+        mbar_init(done, 1);
+        mbar_fence_init();
+        *abort_flag = 0;
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_ptr, tmem_cols);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_ptr);
+
+    if (warp == 0) {
+        if (elect_one_sync()) {
+            prefetch_tensormap(&wmap);
+            prefetch_tensormap(&xmap);
+            int issued = 0;
+            for (; issued < count; ++issued) {
+                const int st = issued % NS;
+                if (issued >= NS) wait_or_abort(empty + st, ((issued / NS) - 1) & 1, abort_flag, status);
+                if (*abort_flag) break;
+                uint8_t* a = sm + st * F::kStageBytes;
+                const int k = (kb0 + issued) * (E4M3 ? kRowBytes : kRowBytes / 2);
+                mbar_arrive_expect_tx(full + st, F::kStageBytes);
+                tma_load_2d(a, &wmap, k, n0, full + st);
+                tma_load_2d(a + 128 * kRowBytes, &xmap, k, m0, full + st);
+            }
+            // loads in flight end before the CTA does (in abort mode the MMA warp
+            // may not have waited for them)
+            for (int i = std::max(0, issued - NS); i < issued; ++i)
+                mbar_wait(full + i % NS, (i / NS) & 1, kPollLimit);
+        }
+    } else if (warp == 1) {
+        if (elect_one_sync()) {
+            constexpr uint32_t idesc = E4M3 ? idesc_e4m3(128, BN) : idesc_bf16(128, BN, false, false);
+            for (int i = 0; i < count; ++i) {
+                const int st = i % NS;
+                wait_or_abort(full + st, (i / NS) & 1, abort_flag, status);
+                if (*abort_flag) break;
+                tc_fence_after_sync();
+                const uint32_t a = smem_addr(sm + st * F::kStageBytes);
+                const uint64_t ad = sdesc_sw128(a, 16, 1024), bd = sdesc_sw128(a + 128 * kRowBytes, 16, 1024);
+                const uint32_t d = tmem + (uint32_t)(i / seg_blocks) * BN;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    mma_step<E4M3, false>(d, ad + 2 * j, bd + 2 * j, idesc, i % seg_blocks != 0 || j != 0);
+                mma_commit(empty + st);
+            }
+            mma_commit(done);
+        }
+    }
+    __syncwarp();
+    wait_or_abort(done, 0, abort_flag, status);
+    tc_fence_after_sync();
+    // this CTA's tile: lane = channel; into shared memory as [token][channel].
+    // Every MMA has read its stages by now, so the stages' memory is free.
+    float* red = reinterpret_cast<float*>(sm);
+    const int segments = (count + seg_blocks - 1) / seg_blocks;
+    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+    const int tokens = min(BN, e.M - m0);
+#pragma unroll 1
+    for (int c = 0; c < BN; c += 16) {
+        if (c >= tokens) break;
+        uint32_t v[16];
+        tmem_ld16_sync(lanes + c, v);
+        for (int s = 1; s < segments; ++s) {
+            uint32_t u[16];
+            tmem_ld16_sync(lanes + s * BN + c, u);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(u[j]));
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) red[(c + j) * 128 + warp * 32 + lane] = __uint_as_float(v[j]);
+    }
+    tc_fence_before_sync();
+    if (splits > 1) cluster_sync();
+    else __syncthreads();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, tmem_cols);
+    }
+
+    const uint32_t red_addr = smem_addr(red);
+    const bool vec = (e.N & 3) == 0;  // rows of y and residual then start on four elements
+    for (int t = rank + warp * splits; t < tokens; t += 4 * splits) {
+        const int m = m0 + t;
+        float v[4];
+        if (vec) {
+            const uint32_t at = red_addr + (uint32_t)(t * 128 + lane * 4) * 4;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int r = 0; r < splits; ++r) {
+                const float4 p = ld_cluster_f4(splits > 1 ? map_rank(at, r) : at);
+                s.x += p.x; s.y += p.y; s.z += p.z; s.w += p.w;
+            }
+            v[0] = s.x; v[1] = s.y; v[2] = s.z; v[3] = s.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t at = red_addr + (uint32_t)(t * 128 + lane + 32 * j) * 4;
+                v[j] = 0.f;
+                for (int r = 0; r < splits; ++r) v[j] += ld_cluster_f1(splits > 1 ? map_rank(at, r) : at);
+            }
+        }
+        const int n = n0 + (vec ? lane * 4 : lane), step = vec ? 1 : 32;
+        const float sx = E4M3 ? e.x_scale[m] : 1.0f;
+        const long long row = (long long)m * e.N;
+        const O* res = static_cast<const O*>(e.residual);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int nj = n + j * step;
+            if (nj >= e.N) continue;
+            if constexpr (E4M3) v[j] = v[j] * sx * __ldg(e.w_scale + nj);
+            if (e.bias) v[j] += __ldg(e.bias + nj);
+            v[j] = activate(v[j], e.act);
+        }
+        O* y = static_cast<O*>(e.y) + row;
+        if (vec) {
+            if (n < e.N) {
+                if (res) {
+                    Packed<O, 4> p;
+                    p.load(res + row + n);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[j] += p.get(j);
+                }
+                Packed<O, 4> p;
+                p.set(v);
+                p.store(y + n);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int nj = n + j * step;
+                if (nj >= e.N) continue;
+                if (res) v[j] += static_cast<float>(res[row + nj]);
+                io<O>::store(y + nj, v[j]);
+            }
+        }
+    }
+    if (splits > 1) cluster_sync();  // no CTA leaves while another reads its tile
+}
+
+template <int BN, bool E4M3, typename O>
+cudaError_t launch_few(const LinearArgs& a, const Epilogue& e, int splits, const LaunchCtx& ctx)
+{
+    using F = Few<BN>;
+    const int es = E4M3 ? 1 : 2;
+    const int kblocks = (int)(((long long)a.K * es + kRowBytes - 1) / kRowBytes);
+    const int tn = (a.N + 127) / 128, tm = (a.M + BN - 1) / BN;
+    const int per = (kblocks + splits - 1) / splits;  // blocks of the longest part
+    // about 512 bf16 products to a segment, as far as the accumulators go
+    const int seg_blocks = std::max(8, (per + F::kMaxSegments - 1) / F::kMaxSegments);
+    const int segments = (per + seg_blocks - 1) / seg_blocks;
+    uint32_t cols = 32;
+    while ((int)cols < segments * BN) cols *= 2;
+    CUtensorMap wmap, xmap;
+    if (!make_map_rows(&wmap, a.w, E4M3, a.K, a.N, (uint64_t)a.K * es, 128) ||
+        !make_map_rows(&xmap, a.x, E4M3, a.K, a.M, (uint64_t)a.x_stride * es, BN))
+        return cudaErrorInvalidValue;
+    auto* kernel = linear_few_kernel<BN, E4M3, O>;
+    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem);
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(splits, tn, tm);
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = F::kSmem;
+    cfg.stream = ctx.stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = splits;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = splits > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, wmap, xmap, e, kblocks, seg_blocks, cols, ctx.status);
+}
+
+template <bool E4M3, typename O>
+cudaError_t few(const LinearArgs& a, const Epilogue& e, const LaunchCtx& ctx)
+{
+    const int BN = a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 ? 64 : 128;
+    const int kblocks = (int)(((long long)a.K * (E4M3 ? 1 : 2) + kRowBytes - 1) / kRowBytes);
+    const long long tiles = (long long)((a.N + 127) / 128) * ((a.M + BN - 1) / BN);
+    // as many parts of K as two CTAs per SM hold at once, of two blocks at least
+    int splits = (int)std::min<long long>(8, 2ll * ctx.num_sms / tiles);
+    splits = std::max(1, std::min(splits, kblocks / 2));
+    switch (BN) {
+    case 16: return launch_few<16, E4M3, O>(a, e, splits, ctx);
+    case 32: return launch_few<32, E4M3, O>(a, e, splits, ctx);
+    case 64: return launch_few<64, E4M3, O>(a, e, splits, ctx);
+    default: return launch_few<128, E4M3, O>(a, e, splits, ctx);
+    }
+}
+
+template <bool E4M3, typename O>
+cudaError_t run(const LinearArgs& a, const LaunchCtx& ctx)
+{
+    const Epilogue e{a.x_scale, a.w_scale, a.bias, a.residual, a.y, a.M, a.N, a.act};
+    return few<E4M3, O>(a, e, ctx);
+}
+
+// TMA addresses rows of 16-byte multiples from 16-byte bases.
+bool tensor_core_rows(const LinearArgs& a)
+{
+    const int unit = a.type == LinearType::bf16 ? 8 : 16;
+    return a.type != LinearType::f32 && aligned_to(a.x, 16) && a.x_stride % unit == 0 && a.K % unit == 0;
+}
+
+}  // namespace
+
+cudaError_t linear(const LinearArgs& a, const LaunchCtx& ctx)
+{
+    if (!tensor_core_rows(a)) return linear_simt(a, ctx);
+    if (a.type == LinearType::e4m3)
+        return a.out_bf16 ? run<true, __nv_bfloat16>(a, ctx) : run<true, float>(a, ctx);
+    return a.out_bf16 ? run<false, __nv_bfloat16>(a, ctx) : run<false, float>(a, ctx);
+}
+
+}  // namespace ssd
