@@ -247,7 +247,7 @@ ssd_status ssd_rms_norm(const void* x, const void* residual, const void* gate, i
  *   residual  [M, N]      `y_dtype` or NULL. May be y itself.
  *   y         [M, N]      `y_dtype`: SSD_F32 or SSD_BF16
  *   dtype     SSD_F32, SSD_BF16 or SSD_E4M3, of both operands
- *   Sizes: M, N >= 0 (0 is a no-op), K >= 1; N, K <= 2^20. x needs its
+ *   Sizes: M, N >= 0 (0 is a no-op), K >= 1; M <= 2^30; N, K <= 2^20. x needs its
  *   element's alignment only; every other pointer is 16-byte aligned.
  */
 ssd_status ssd_linear(const void* x, int64_t x_stride, const void* w, const float* x_scale,

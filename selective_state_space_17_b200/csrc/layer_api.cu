@@ -143,7 +143,7 @@ ssd_status ssd_linear(const void* x, int64_t x_stride, const void* w, const floa
     if (dtype != SSD_E4M3 && !io_dtype(dtype)) return SSD_ERR_INVALID_ARG;
     if (!io_dtype(y_dtype)) return SSD_ERR_INVALID_ARG;
     if (act != SSD_ACT_NONE && act != SSD_ACT_SILU && act != SSD_ACT_GELU) return SSD_ERR_INVALID_ARG;
-    if (N > (1 << 20) || K > (1 << 20)) return SSD_ERR_UNSUPPORTED;
+    if (M > (1 << 30) || N > (1 << 20) || K > (1 << 20)) return SSD_ERR_UNSUPPORTED;
     if (M == 0 || N == 0) return SSD_OK;
     if (!x || !w || !y) return SSD_ERR_INVALID_ARG;
     if ((dtype == SSD_E4M3) != (x_scale != nullptr) || (dtype == SSD_E4M3) != (w_scale != nullptr))

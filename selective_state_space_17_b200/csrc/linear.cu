@@ -273,11 +273,289 @@ cudaError_t few(const LinearArgs& a, const Epilogue& e, const LaunchCtx& ctx)
     }
 }
 
+// ------------------------------------------------------------ many tokens
+
+// A pair of CTAs computes 256 tokens x BN channels: each stages its own 128
+// tokens and half of the channels, and one thread of the leader issues
+// tcgen05.mma.cta_group::2 for both, so an operand byte is read from L2 and
+// stored to shared memory once per pair instead of once per CTA. Accumulators
+// (128 lanes = tokens, BN columns in each CTA) take turns in TMEM, so the
+// epilogue of one runs under the products of the next.
+//
+// SEG (fp32 outputs): the epilogue warps hold the tile in registers and add up
+// accumulators of at most kSegBlocks K blocks with rounded additions, against
+// the bias of the tensor cores' truncated ones (see linear_few_kernel); a bf16
+// output's own rounding, 2^-9, hides that bias.
+template <int BN>
+struct Many {
+    static constexpr int kBRows = BN / 2;
+    static constexpr int kStageBytes = (128 + kBRows) * kRowBytes;
+    static constexpr int kStages = (200 * 1024) / kStageBytes;
+    static constexpr int kSmem = 1024 + kStages * kStageBytes + 512;
+    static constexpr int kBuffers = 512 / BN;
+    static constexpr int kEpiWarps = 8;
+    static constexpr int kThreads = 128 + 32 * kEpiWarps;
+    static constexpr int kSegBlocks = 8;
+};
+
+// Stores the 32 columns c .. c + 31 (n0 + c is the channel) of one token's row.
+template <bool E4M3, typename O>
+__device__ __forceinline__ void store_row32(const Epilogue& e, const float* acc, int m, int n, float sx, int width)
+{
+    const long long at = (long long)m * e.N + n;
+    O* y = static_cast<O*>(e.y) + at;
+    const O* res = static_cast<const O*>(e.residual);
+    if (width > 1 && n + 32 <= e.N) {
+        constexpr int V = 16 / (int)sizeof(O);
+#pragma unroll
+        for (int c = 0; c < 32; c += V) {
+            float v[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                v[j] = acc[c + j];
+                if constexpr (E4M3) v[j] = v[j] * sx * __ldg(e.w_scale + n + c + j);
+                if (e.bias) v[j] += __ldg(e.bias + n + c + j);
+                v[j] = activate(v[j], e.act);
+            }
+            if (res) {
+                Packed<O, V> p;
+                p.load(res + at + c);
+#pragma unroll
+                for (int j = 0; j < V; ++j) v[j] += p.get(j);
+            }
+            Packed<O, V> p;
+            p.set(v);
+            p.store(y + c);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            if (n + j >= e.N) break;
+            float v = acc[j];
+            if constexpr (E4M3) v = v * sx * __ldg(e.w_scale + n + j);
+            if (e.bias) v += __ldg(e.bias + n + j);
+            v = activate(v, e.act);
+            if (res) v += static_cast<float>(res[at + j]);
+            io<O>::store(y + j, v);
+        }
+    }
+}
+
+struct Tiles {
+    int tm, tn;    // tiles along the tokens and the channels
+    int group;     // tile rows walked together
+    long long all;
+};
+
+// Tiles in groups of `group` rows, column by column within a group, so that the
+// tiles in flight at once share operands in L2.
+__device__ __forceinline__ void tile_at(const Tiles& t, long long i, int& im, int& in)
+{
+    const long long per = (long long)t.group * t.tn;
+    const int g = (int)(i / per);
+    const int rows = min(t.group, t.tm - g * t.group);
+    const int r = (int)(i - g * per);
+    im = g * t.group + r % rows;
+    in = r / rows;
+}
+
+template <int BN, bool E4M3, typename O, bool SEG>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Many<BN>::kThreads, 1)
+linear_many_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+                   const Epilogue e, const Tiles tiles, int kblocks, int width, unsigned int* status)
+{
+    using T = Many<BN>;
+    constexpr int NS = T::kStages, NB = T::kBuffers;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(sm + NS * T::kStageBytes);  // leader's: both CTAs' loads
+    uint64_t* empty = full + NS;          // each CTA's
+    uint64_t* acc_full = empty + NS;      // each CTA's
+    uint64_t* acc_empty = acc_full + NB;  // leader's: both CTAs' epilogue warps
+    uint64_t* drained = acc_empty + NB;   // each CTA's: every product issued has completed
+    uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(drained + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_ptr + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int seg = SEG ? T::kSegBlocks : kblocks;  // K blocks of one accumulator
+    const int segs = SEG ? (kblocks + seg - 1) / seg : 1;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, 1);
+        }
+        for (int i = 0; i < NB; ++i) {
+            mbar_init(acc_full + i, 1);
+            mbar_init(acc_empty + i, 2 * T::kEpiWarps);
+        }
+        mbar_init(drained, 1);
+        mbar_fence_init();
+        *abort_flag = 0;
+    }
+    if (warp == 2) tmem_alloc_pair(tmem_ptr, 512);
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_sync();  // barriers of both CTAs are set up
+    tc_fence_after_sync();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_ptr);
+
+    if (warp == 0) {
+        if (elect_one_sync()) {
+            prefetch_tensormap(&wmap);
+            prefetch_tensormap(&xmap);
+            long long it = 0;
+            for (long long i = pair; i < tiles.all && !*abort_flag; i += pairs) {
+                int im, in;
+                tile_at(tiles, i, im, in);
+                const int m = im * 256 + (int)rank * 128, n = in * BN + (int)rank * T::kBRows;
+                for (int kb = 0; kb < kblocks; ++kb, ++it) {
+                    const int st = (int)(it % NS);
+                    if (it >= NS) wait_or_abort(empty + st, (uint32_t)((it / NS) - 1) & 1, abort_flag, status);
+                    if (*abort_flag) break;
+                    uint8_t* a = sm + st * T::kStageBytes;
+                    const int k = kb * (E4M3 ? kRowBytes : kRowBytes / 2);
+                    // the leader's barrier counts both CTAs' bytes
+                    if (rank == 0) mbar_arrive_expect_tx(full + st, 2 * T::kStageBytes);
+                    const uint32_t bar = map_rank(smem_addr(full + st), 0);
+                    tma_load_2d_pair(a, &xmap, k, m, bar);
+                    tma_load_2d_pair(a + 128 * kRowBytes, &wmap, k, n, bar);
+                }
+            }
+            // every stage loaded has been read by the MMAs: none is in flight when
+            // the CTA ends, nor a commit's arrival on this CTA's barriers
+            for (long long j = it > NS ? it - NS : 0; j < it; ++j)
+                mbar_wait(empty + j % NS, (uint32_t)(j / NS) & 1, kPollLimit);
+        }
+    } else if (warp == 1 && rank != 0) {
+        if (elect_one_sync()) wait_or_abort(drained, 0, abort_flag, status);
+    } else if (warp == 1) {
+        if (elect_one_sync()) {
+            constexpr uint32_t idesc = E4M3 ? idesc_e4m3(256, BN) : idesc_bf16(256, BN, false, false);
+            long long it = 0, unit = 0;
+            for (long long i = pair; i < tiles.all && !*abort_flag; i += pairs) {
+                for (int kb = 0; kb < kblocks; ++kb, ++it) {
+                    const int buf = (int)(unit % NB);
+                    const bool first = kb % seg == 0;
+                    if (first) {
+                        if (unit >= NB)
+                            wait_or_abort(acc_empty + buf, (uint32_t)((unit / NB) - 1) & 1, abort_flag, status);
+                        tc_fence_after_sync();
+                    }
+                    const int st = (int)(it % NS);
+                    wait_or_abort(full + st, (uint32_t)(it / NS) & 1, abort_flag, status);
+                    if (*abort_flag) break;
+                    tc_fence_after_sync();
+                    const uint32_t a = smem_addr(sm + st * T::kStageBytes);
+                    const uint64_t ad = sdesc_sw128(a, 16, 1024), bd = sdesc_sw128(a + 128 * kRowBytes, 16, 1024);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        mma_step<E4M3, true>(tmem + buf * BN, ad + 2 * j, bd + 2 * j, idesc, !first || j != 0);
+                    mma_commit_pair(empty + st);
+                    if (kb % seg == seg - 1 || kb == kblocks - 1) {
+                        mma_commit_pair(acc_full + buf);
+                        ++unit;
+                    }
+                }
+            }
+            mma_commit_pair(drained);
+            mbar_wait(drained, 0, kPollLimit);
+        }
+    } else if (warp >= 4) {
+        // two warps to each quadrant of 32 lanes, half of the columns each
+        const int quad = warp & 3, half = (warp - 4) >> 2;
+        constexpr int kCols = BN / 2;
+        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + half * kCols;
+        long long unit = 0;
+        for (long long i = pair; i < tiles.all && !*abort_flag; i += pairs) {
+            int im, in;
+            tile_at(tiles, i, im, in);
+            const int m = im * 256 + (int)rank * 128 + quad * 32 + lane;
+            const int n = in * BN + half * kCols;
+            const float sx = E4M3 && m < e.M ? __ldg(e.x_scale + m) : 1.0f;
+            float sum[SEG ? kCols : 1];
+            for (int s = 0; s < segs; ++s, ++unit) {
+                const int buf = (int)(unit % NB);
+                wait_or_abort(acc_full + buf, (uint32_t)(unit / NB) & 1, abort_flag, status);
+                tc_fence_after_sync();
+                if constexpr (SEG) {
+#pragma unroll
+                    for (int c = 0; c < kCols; c += 16) {
+                        uint32_t v[16];
+                        tmem_ld16_sync(lanes + buf * BN + c, v);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            sum[c + j] = s == 0 ? __uint_as_float(v[j]) : sum[c + j] + __uint_as_float(v[j]);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < kCols; c += 32) {
+                        uint32_t v[32];
+                        tmem_ld32_sync(lanes + buf * BN + c, v);
+                        float f[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
+                        if (m < e.M && !*abort_flag) store_row32<E4M3, O>(e, f, m, n + c, sx, width);
+                    }
+                }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(map_rank(smem_addr(acc_empty + buf), 0));
+            }
+            if constexpr (SEG) {
+                if (m < e.M && !*abort_flag) {
+#pragma unroll
+                    for (int c = 0; c < kCols; c += 32) store_row32<E4M3, O>(e, sum + c, m, n + c, sx, width);
+                }
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before_sync();
+    // all of the pair's products have been read and all arrivals on its barriers
+    // have landed before either CTA ends
+    cluster_sync();
+    tc_fence_after_sync();
+    if (warp == 2) tmem_dealloc_pair(tmem, 512);
+}
+
+template <int BN, bool E4M3, typename O, bool SEG>
+cudaError_t launch_many(const LinearArgs& a, const Epilogue& e, const LaunchCtx& ctx)
+{
+    using T = Many<BN>;
+    const int es = E4M3 ? 1 : 2;
+    const int kblocks = (int)(((long long)a.K * es + kRowBytes - 1) / kRowBytes);
+    Tiles t;
+    t.tm = (int)(((long long)a.M + 255) / 256);
+    t.tn = (a.N + BN - 1) / BN;
+    t.group = 8;
+    t.all = (long long)t.tm * t.tn;
+    CUtensorMap wmap, xmap;
+    if (!make_map_rows(&wmap, a.w, E4M3, a.K, a.N, (uint64_t)a.K * es, T::kBRows) ||
+        !make_map_rows(&xmap, a.x, E4M3, a.K, a.M, (uint64_t)a.x_stride * es, 128))
+        return cudaErrorInvalidValue;
+    auto* kernel = linear_many_kernel<BN, E4M3, O, SEG>;
+    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
+    if (err != cudaSuccess) return err;
+    const int width = a.N % (16 / (int)sizeof(O)) == 0 ? 16 : 1;
+    const int pairs = (int)std::min<long long>(t.all, ctx.num_sms / 2);
+    kernel<<<2 * pairs, T::kThreads, T::kSmem, ctx.stream>>>(wmap, xmap, e, t, kblocks, width, ctx.status);
+    return cudaGetLastError();
+}
+
+template <bool E4M3, typename O>
+cudaError_t many(const LinearArgs& a, const Epilogue& e, const LaunchCtx& ctx)
+{
+    if constexpr (sizeof(O) == 4) return launch_many<128, E4M3, O, true>(a, e, ctx);
+    else return launch_many<256, E4M3, O, false>(a, e, ctx);
+}
+
 template <bool E4M3, typename O>
 cudaError_t run(const LinearArgs& a, const LaunchCtx& ctx)
 {
     const Epilogue e{a.x_scale, a.w_scale, a.bias, a.residual, a.y, a.M, a.N, a.act};
-    return few<E4M3, O>(a, e, ctx);
+    return a.M >= 1024 ? many<E4M3, O>(a, e, ctx) : few<E4M3, O>(a, e, ctx);
 }
 
 // TMA addresses rows of 16-byte multiples from 16-byte bases.

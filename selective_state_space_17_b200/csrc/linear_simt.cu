@@ -23,7 +23,7 @@ __global__ void __launch_bounds__(256) linear_simt_kernel(LinearArgs a)
     __shared__ float xs[BK][BM + 4], ws[BK][BN + 4];
     const T* x = static_cast<const T*>(a.x);
     const T* w = static_cast<const T*>(a.w);
-    const int m0 = blockIdx.y * BM, n0 = blockIdx.x * BN;
+    const int m0 = blockIdx.x * BM, n0 = blockIdx.y * BN;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     float acc[4][4] = {};
     for (int k0 = 0; k0 < a.K; k0 += BK) {
@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(256) linear_simt_kernel(LinearArgs a)
 template <typename T>
 cudaError_t launch(const LinearArgs& a, const LaunchCtx& ctx)
 {
-    const dim3 grid((a.N + BN - 1) / BN, (a.M + BM - 1) / BM);
+    const dim3 grid((a.M + BM - 1) / BM, (a.N + BN - 1) / BN);
     if (a.out_bf16) linear_simt_kernel<T, __nv_bfloat16><<<grid, 256, 0, ctx.stream>>>(a);
     else linear_simt_kernel<T, float><<<grid, 256, 0, ctx.stream>>>(a);
     return cudaGetLastError();

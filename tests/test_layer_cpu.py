@@ -66,7 +66,7 @@ def linear(lib, **kw):
 @pytest.mark.parametrize("kw,want", [
     (dict(M=-1), INVALID), (dict(N=-1), INVALID), (dict(K=0), INVALID), (dict(act=3), INVALID),
     (dict(dtype=3), INVALID), (dict(ydtype=E4M3), INVALID), (dict(ydtype=7), INVALID),
-    (dict(N=(1 << 20) + 1), UNSUPPORTED), (dict(K=(1 << 20) + 1, x_stride=1 << 21), UNSUPPORTED),
+    (dict(M=(1 << 30) + 1), UNSUPPORTED), (dict(N=(1 << 20) + 1), UNSUPPORTED), (dict(K=(1 << 20) + 1, x_stride=1 << 21), UNSUPPORTED),
     (dict(x=None), INVALID), (dict(w=None), INVALID), (dict(y=None), INVALID),
     (dict(xs=P(3)), INVALID), (dict(dtype=E4M3, xs=P(3)), INVALID), (dict(dtype=E4M3, ws=P(3)), INVALID),
     (dict(x_stride=31), INVALID), (dict(x=P(0) + 1), MISALIGNED), (dict(w=P(1) + 8), MISALIGNED),
