@@ -298,45 +298,90 @@ struct Many {
     static constexpr int kSegBlocks = 8;
 };
 
-// Stores the 32 columns c .. c + 31 (n0 + c is the channel) of one token's row.
-template <bool E4M3, typename O>
-__device__ __forceinline__ void store_row32(const Epilogue& e, const float* acc, int m, int n, float sx, int width)
+// 32 bytes of one row (rows that allow it start on 32 bytes).
+__device__ __forceinline__ void st32(void* p, const uint32_t* w)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+}
+__device__ __forceinline__ void ld32(const void* p, uint32_t* w)
+{
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p) : "memory");
+}
+
+// Four consecutive fp32 values that start on 16 bytes.
+__device__ __forceinline__ void ldg4(const float* p, float* v)
+{
+    const float4 f = __ldg(reinterpret_cast<const float4*>(p));
+    v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+}
+
+// The epilogue of 32 channels n .. n + 31 (n a multiple of 32) of token m: the
+// thread's 32 accumulator columns to y. WIDE: rows start on 32 bytes.
+template <bool E4M3, typename O, bool WIDE>
+__device__ __forceinline__ void store_row32(const Epilogue& e, float* v, int m, int n, float sx)
 {
     const long long at = (long long)m * e.N + n;
     O* y = static_cast<O*>(e.y) + at;
     const O* res = static_cast<const O*>(e.residual);
-    if (width > 1 && n + 32 <= e.N) {
-        constexpr int V = 16 / (int)sizeof(O);
+    if (WIDE && n + 32 <= e.N) {
+        constexpr int kWords = 32 * (int)sizeof(O) / 4;
+        uint32_t r[kWords];
+        if (res) {
 #pragma unroll
-        for (int c = 0; c < 32; c += V) {
-            float v[V];
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                v[j] = acc[c + j];
-                if constexpr (E4M3) v[j] = v[j] * sx * __ldg(e.w_scale + n + c + j);
-                if (e.bias) v[j] += __ldg(e.bias + n + c + j);
-                v[j] = activate(v[j], e.act);
-            }
-            if (res) {
-                Packed<O, V> p;
-                p.load(res + at + c);
-#pragma unroll
-                for (int j = 0; j < V; ++j) v[j] += p.get(j);
-            }
-            Packed<O, V> p;
-            p.set(v);
-            p.store(y + c);
+            for (int i = 0; i < kWords; i += 8) ld32(res + at + i * 4 / (int)sizeof(O), r + i);
         }
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+            float b[4];
+            if constexpr (E4M3) {
+                ldg4(e.w_scale + n + c, b);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[c + j] = v[c + j] * sx * b[j];
+            }
+            if (e.bias) {
+                ldg4(e.bias + n + c, b);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[c + j] += b[j];
+            }
+        }
+        if (e.act == SSD_ACT_SILU) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = silu_f(v[j]);
+        } else if (e.act == SSD_ACT_GELU) {
+#pragma unroll 1
+            for (int c = 0; c < 32; c += 8)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    // a rotation by 8 keeps the indexes constants: the loop is
+                    // rolled for the sake of erfc's length
+                    const float t = gelu_f(v[j]);
+                    v[j] = v[j + 8]; v[j + 8] = v[j + 16]; v[j + 16] = v[j + 24]; v[j + 24] = t;
+                }
+        }
+        Packed<O, 32> p;
+        if (res) {
+            Packed<O, 32> q;
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) q.w[i] = r[i];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] += q.get(j);
+        }
+        p.set(v);
+#pragma unroll
+        for (int i = 0; i < kWords; i += 8) st32(y + i * 4 / (int)sizeof(O), p.w + i);
     } else {
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
             if (n + j >= e.N) break;
-            float v = acc[j];
-            if constexpr (E4M3) v = v * sx * __ldg(e.w_scale + n + j);
-            if (e.bias) v += __ldg(e.bias + n + j);
-            v = activate(v, e.act);
-            if (res) v += static_cast<float>(res[at + j]);
-            io<O>::store(y + j, v);
+            float t = v[j];
+            if constexpr (E4M3) t = t * sx * __ldg(e.w_scale + n + j);
+            if (e.bias) t += __ldg(e.bias + n + j);
+            t = activate(t, e.act);
+            if (res) t += static_cast<float>(res[at + j]);
+            io<O>::store(y + j, t);
         }
     }
 }
@@ -359,10 +404,10 @@ __device__ __forceinline__ void tile_at(const Tiles& t, long long i, int& im, in
     in = r / rows;
 }
 
-template <int BN, bool E4M3, typename O, bool SEG>
+template <int BN, bool E4M3, typename O, bool SEG, bool WIDE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Many<BN>::kThreads, 1)
 linear_many_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
-                   const Epilogue e, const Tiles tiles, int kblocks, int width, unsigned int* status)
+                   const Epilogue e, const Tiles tiles, int kblocks, unsigned int* status)
 {
     using T = Many<BN>;
     constexpr int NS = T::kStages, NB = T::kBuffers;
@@ -496,7 +541,7 @@ linear_many_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                         float f[32];
 #pragma unroll
                         for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
-                        if (m < e.M && !*abort_flag) store_row32<E4M3, O>(e, f, m, n + c, sx, width);
+                        if (m < e.M && !*abort_flag) store_row32<E4M3, O, WIDE>(e, f, m, n + c, sx);
                     }
                 }
                 tc_fence_before_sync();
@@ -506,7 +551,7 @@ linear_many_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             if constexpr (SEG) {
                 if (m < e.M && !*abort_flag) {
 #pragma unroll
-                    for (int c = 0; c < kCols; c += 32) store_row32<E4M3, O>(e, sum + c, m, n + c, sx, width);
+                    for (int c = 0; c < kCols; c += 32) store_row32<E4M3, O, WIDE>(e, sum + c, m, n + c, sx);
                 }
             }
         }
@@ -535,12 +580,12 @@ cudaError_t launch_many(const LinearArgs& a, const Epilogue& e, const LaunchCtx&
     if (!make_map_rows(&wmap, a.w, E4M3, a.K, a.N, (uint64_t)a.K * es, T::kBRows) ||
         !make_map_rows(&xmap, a.x, E4M3, a.K, a.M, (uint64_t)a.x_stride * es, 128))
         return cudaErrorInvalidValue;
-    auto* kernel = linear_many_kernel<BN, E4M3, O, SEG>;
+    const bool wide = (long long)a.N * sizeof(O) % 32 == 0 && aligned_to(a.y, 32) && aligned_to(a.residual, 32);
+    auto* kernel = wide ? linear_many_kernel<BN, E4M3, O, SEG, true> : linear_many_kernel<BN, E4M3, O, SEG, false>;
     cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
     if (err != cudaSuccess) return err;
-    const int width = a.N % (16 / (int)sizeof(O)) == 0 ? 16 : 1;
     const int pairs = (int)std::min<long long>(t.all, ctx.num_sms / 2);
-    kernel<<<2 * pairs, T::kThreads, T::kSmem, ctx.stream>>>(wmap, xmap, e, t, kblocks, width, ctx.status);
+    kernel<<<2 * pairs, T::kThreads, T::kSmem, ctx.stream>>>(wmap, xmap, e, t, kblocks, ctx.status);
     return cudaGetLastError();
 }
 
