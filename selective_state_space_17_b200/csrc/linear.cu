@@ -282,18 +282,22 @@ cudaError_t few(const LinearArgs& a, const Epilogue& e, const LaunchCtx& ctx)
 // (128 lanes = tokens, BN columns in each CTA) take turns in TMEM, so the
 // epilogue of one runs under the products of the next.
 //
-// SEG (fp32 outputs): the epilogue warps hold the tile in registers and add up
+// SEG (fp32 outputs of bf16 operands): the epilogue warps hold the tile in registers and add up
 // accumulators of at most kSegBlocks K blocks with rounded additions, against
-// the bias of the tensor cores' truncated ones (see linear_few_kernel); a bf16
-// output's own rounding, 2^-9, hides that bias.
-template <int BN>
+// the bias of the tensor cores' truncated ones (see linear_few_kernel). A bf16
+// output's own rounding hides that bias, and products of e4m3 values, with eight
+// significant bits at most, lose next to nothing (measured 1e-8 at K = 5120).
+template <int BN, bool SEG>
 struct Many {
     static constexpr int kBRows = BN / 2;
     static constexpr int kStageBytes = (128 + kBRows) * kRowBytes;
     static constexpr int kStages = (200 * 1024) / kStageBytes;
     static constexpr int kSmem = 1024 + kStages * kStageBytes + 512;
     static constexpr int kBuffers = 512 / BN;
-    static constexpr int kEpiWarps = 8;
+    // warps of a lane quadrant share its columns: with SEG each holds its 64 in
+    // registers, without it 128 in passing
+    static constexpr int kParts = SEG ? BN / 64 : 2;
+    static constexpr int kEpiWarps = 4 * kParts;
     static constexpr int kThreads = 128 + 32 * kEpiWarps;
     static constexpr int kSegBlocks = 8;
 };
@@ -318,23 +322,23 @@ __device__ __forceinline__ void ldg4(const float* p, float* v)
     v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
 }
 
-// The epilogue of 32 channels n .. n + 31 (n a multiple of 32) of token m: the
-// thread's 32 accumulator columns to y. WIDE: rows start on 32 bytes.
-template <bool E4M3, typename O, bool WIDE>
-__device__ __forceinline__ void store_row32(const Epilogue& e, float* v, int m, int n, float sx)
+// The epilogue of CH channels from n (a multiple of CH) of token m: the thread's
+// accumulator columns to y. WIDE: rows start on 32 bytes.
+template <int CH, bool E4M3, typename O, bool WIDE>
+__device__ __forceinline__ void store_row(const Epilogue& e, const void* residual, float* v, int m, int n, float sx)
 {
     const long long at = (long long)m * e.N + n;
     O* y = static_cast<O*>(e.y) + at;
-    const O* res = static_cast<const O*>(e.residual);
-    if (WIDE && n + 32 <= e.N) {
-        constexpr int kWords = 32 * (int)sizeof(O) / 4;
+    const O* res = static_cast<const O*>(residual);
+    if (WIDE && n + CH <= e.N) {
+        constexpr int kWords = CH * (int)sizeof(O) / 4;
         uint32_t r[kWords];
         if (res) {
 #pragma unroll
             for (int i = 0; i < kWords; i += 8) ld32(res + at + i * 4 / (int)sizeof(O), r + i);
         }
 #pragma unroll
-        for (int c = 0; c < 32; c += 4) {
+        for (int c = 0; c < CH; c += 4) {
             float b[4];
             if constexpr (E4M3) {
                 ldg4(e.w_scale + n + c, b);
@@ -349,32 +353,35 @@ __device__ __forceinline__ void store_row32(const Epilogue& e, float* v, int m, 
         }
         if (e.act == SSD_ACT_SILU) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = silu_f(v[j]);
+            for (int j = 0; j < CH; ++j) v[j] = silu_f(v[j]);
         } else if (e.act == SSD_ACT_GELU) {
+            // rolled for the sake of erfc's length; rotating the values by 8 keeps
+            // their indexes constants
 #pragma unroll 1
-            for (int c = 0; c < 32; c += 8)
+            for (int c = 0; c < CH; c += 8) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    // a rotation by 8 keeps the indexes constants: the loop is
-                    // rolled for the sake of erfc's length
                     const float t = gelu_f(v[j]);
-                    v[j] = v[j + 8]; v[j + 8] = v[j + 16]; v[j + 16] = v[j + 24]; v[j + 24] = t;
+#pragma unroll
+                    for (int i = j; i + 8 < CH; i += 8) v[i] = v[i + 8];
+                    v[CH - 8 + j] = t;
                 }
+            }
         }
-        Packed<O, 32> p;
+        Packed<O, CH> p;
         if (res) {
-            Packed<O, 32> q;
+            Packed<O, CH> q;
 #pragma unroll
             for (int i = 0; i < kWords; ++i) q.w[i] = r[i];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] += q.get(j);
+            for (int j = 0; j < CH; ++j) v[j] += q.get(j);
         }
         p.set(v);
 #pragma unroll
         for (int i = 0; i < kWords; i += 8) st32(y + i * 4 / (int)sizeof(O), p.w + i);
     } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
+        for (int j = 0; j < CH; ++j) {
             if (n + j >= e.N) break;
             float t = v[j];
             if constexpr (E4M3) t = t * sx * __ldg(e.w_scale + n + j);
@@ -405,11 +412,11 @@ __device__ __forceinline__ void tile_at(const Tiles& t, long long i, int& im, in
 }
 
 template <int BN, bool E4M3, typename O, bool SEG, bool WIDE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Many<BN>::kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Many<BN, SEG>::kThreads, 1)
 linear_many_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                    const Epilogue e, const Tiles tiles, int kblocks, unsigned int* status)
 {
-    using T = Many<BN>;
+    using T = Many<BN, SEG>;
     constexpr int NS = T::kStages, NB = T::kBuffers;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -508,18 +515,32 @@ linear_many_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             mbar_wait(drained, 0, kPollLimit);
         }
     } else if (warp >= 4) {
-        // two warps to each quadrant of 32 lanes, half of the columns each
-        const int quad = warp & 3, half = (warp - 4) >> 2;
-        constexpr int kCols = BN / 2;
-        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + half * kCols;
+        // each quadrant of 32 lanes belongs to the warps of its number mod 4
+        const int quad = warp & 3, part = (warp - 4) >> 2;
+        constexpr int kCols = BN / T::kParts;
+        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + part * kCols;
         long long unit = 0;
         for (long long i = pair; i < tiles.all && !*abort_flag; i += pairs) {
             int im, in;
             tile_at(tiles, i, im, in);
             const int m = im * 256 + (int)rank * 128 + quad * 32 + lane;
-            const int n = in * BN + half * kCols;
+            const int n = in * BN + part * kCols;
             const float sx = E4M3 && m < e.M ? __ldg(e.x_scale + m) : 1.0f;
             float sum[SEG ? kCols : 1];
+            // without an activation the sum may begin with the residual, which is
+            // then read while the first products are under way
+            const bool early = SEG && WIDE && e.residual && e.act == SSD_ACT_NONE && n + kCols <= e.N;
+            if constexpr (SEG) {
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) sum[c] = 0.0f;
+                if constexpr (WIDE) {
+                    if (early && m < e.M) {
+                        const O* res = static_cast<const O*>(e.residual) + (long long)m * e.N + n;
+#pragma unroll
+                        for (int c = 0; c < kCols; c += 8) ld32(res + c, reinterpret_cast<uint32_t*>(sum) + c);
+                    }
+                }
+            }
             for (int s = 0; s < segs; ++s, ++unit) {
                 const int buf = (int)(unit % NB);
                 wait_or_abort(acc_full + buf, (uint32_t)(unit / NB) & 1, abort_flag, status);
@@ -531,7 +552,7 @@ linear_many_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                         tmem_ld16_sync(lanes + buf * BN + c, v);
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
-                            sum[c + j] = s == 0 ? __uint_as_float(v[j]) : sum[c + j] + __uint_as_float(v[j]);
+                            sum[c + j] += __uint_as_float(v[j]);
                     }
                 } else {
 #pragma unroll 1
@@ -541,7 +562,7 @@ linear_many_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                         float f[32];
 #pragma unroll
                         for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
-                        if (m < e.M && !*abort_flag) store_row32<E4M3, O, WIDE>(e, f, m, n + c, sx);
+                        if (m < e.M && !*abort_flag) store_row<32, E4M3, O, WIDE>(e, e.residual, f, m, n + c, sx);
                     }
                 }
                 tc_fence_before_sync();
@@ -551,7 +572,8 @@ linear_many_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             if constexpr (SEG) {
                 if (m < e.M && !*abort_flag) {
 #pragma unroll
-                    for (int c = 0; c < kCols; c += 32) store_row32<E4M3, O, WIDE>(e, sum + c, m, n + c, sx);
+                    for (int c = 0; c < kCols; c += 8)
+                        store_row<8, E4M3, O, WIDE>(e, early ? nullptr : e.residual, sum + c, m, n + c, sx);
                 }
             }
         }
@@ -568,7 +590,7 @@ linear_many_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
 template <int BN, bool E4M3, typename O, bool SEG>
 cudaError_t launch_many(const LinearArgs& a, const Epilogue& e, const LaunchCtx& ctx)
 {
-    using T = Many<BN>;
+    using T = Many<BN, SEG>;
     const int es = E4M3 ? 1 : 2;
     const int kblocks = (int)(((long long)a.K * es + kRowBytes - 1) / kRowBytes);
     Tiles t;
@@ -592,8 +614,7 @@ cudaError_t launch_many(const LinearArgs& a, const Epilogue& e, const LaunchCtx&
 template <bool E4M3, typename O>
 cudaError_t many(const LinearArgs& a, const Epilogue& e, const LaunchCtx& ctx)
 {
-    if constexpr (sizeof(O) == 4) return launch_many<128, E4M3, O, true>(a, e, ctx);
-    else return launch_many<256, E4M3, O, false>(a, e, ctx);
+    return launch_many<256, E4M3, O, sizeof(O) == 4 && !E4M3>(a, e, ctx);
 }
 
 template <bool E4M3, typename O>
