@@ -339,6 +339,12 @@ void ssd_set_fault_injection(int skip_publish);
  * either kernel. */
 void ssd_set_forward_variant(int variant);
 
+/* Test hook: which kernel ssd_linear uses. 0 (the default) picks the fastest
+ * for the sizes, 1 forces the SIMT kernel, 2 the tensor-core kernel for few
+ * tokens, 3 the one for many (operands that TMA cannot address take the SIMT
+ * kernel all the same). Other values restore 0. */
+void ssd_set_linear_variant(int variant);
+
 #ifdef __cplusplus
 }
 #endif

@@ -65,6 +65,7 @@ struct LinearArgs {
 };
 cudaError_t linear(const LinearArgs& a, const LaunchCtx& ctx);       // the tensor cores where they can
 cudaError_t linear_simt(const LinearArgs& a, const LaunchCtx& ctx);  // any operands
+void set_linear_variant(int variant);
 
 inline bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 

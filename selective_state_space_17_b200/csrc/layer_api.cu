@@ -170,6 +170,8 @@ ssd_status ssd_linear(const void* x, int64_t x_stride, const void* w, const floa
     return launched(linear(a, ctx));
 }
 
+void ssd_set_linear_variant(int variant) { set_linear_variant(variant); }
+
 ssd_status ssd_conv(const void* u, int64_t u_batch_stride, int64_t u_row_stride, const float* weight,
                     const float* bias, const void* dt_raw, int64_t dt_batch_stride,
                     int64_t dt_row_stride, const float* dt_bias, const void* initial_state, void* x,

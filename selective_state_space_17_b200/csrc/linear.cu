@@ -13,6 +13,7 @@
 // the 128-byte swizzle; one tcgen05.mma takes 32 bytes of each row, whatever
 // the type, so the two types share all but the instruction.
 #include <algorithm>
+#include <atomic>
 
 #include "layer.cuh"
 #include "sm100_mma.cuh"
@@ -21,6 +22,8 @@ namespace ssd {
 namespace {
 
 using namespace sm100;
+
+std::atomic<int> g_variant{0};  // test hook: 0 automatic, 1 SIMT, 2 few tokens, 3 many tokens
 
 constexpr int kRowBytes = 128;  // bytes of an operand row in one stage
 
@@ -621,7 +624,8 @@ template <bool E4M3, typename O>
 cudaError_t run(const LinearArgs& a, const LaunchCtx& ctx)
 {
     const Epilogue e{a.x_scale, a.w_scale, a.bias, a.residual, a.y, a.M, a.N, a.act};
-    return a.M >= 1024 ? many<E4M3, O>(a, e, ctx) : few<E4M3, O>(a, e, ctx);
+    const bool use_many = g_variant ? g_variant == 3 : a.M >= 1024;
+    return use_many ? many<E4M3, O>(a, e, ctx) : few<E4M3, O>(a, e, ctx);
 }
 
 // TMA addresses rows of 16-byte multiples from 16-byte bases.
@@ -633,9 +637,11 @@ bool tensor_core_rows(const LinearArgs& a)
 
 }  // namespace
 
+void set_linear_variant(int variant) { g_variant = variant >= 0 && variant <= 3 ? variant : 0; }
+
 cudaError_t linear(const LinearArgs& a, const LaunchCtx& ctx)
 {
-    if (!tensor_core_rows(a)) return linear_simt(a, ctx);
+    if (!tensor_core_rows(a) || g_variant == 1) return linear_simt(a, ctx);
     if (a.type == LinearType::e4m3)
         return a.out_bf16 ? run<true, __nv_bfloat16>(a, ctx) : run<true, float>(a, ctx);
     return a.out_bf16 ? run<false, __nv_bfloat16>(a, ctx) : run<false, float>(a, ctx);

@@ -30,20 +30,29 @@ lib.ssd_conv.restype = _i
 lib.ssd_conv_step.argtypes = [_vp, _i64, _vp, _vp, _vp, _i64] + [_vp] * 6 + [_i] * 8 + [_vp]
 lib.ssd_conv_step.restype = _i
 
+lib.ssd_set_linear_variant.argtypes = [_i]
+lib.ssd_set_linear_variant.restype = None
+
 _F32, _BF16, _E4M3 = torch.float32, torch.bfloat16, torch.float8_e4m3fn
 _IO = {_F32: SSD_F32, _BF16: SSD_BF16}
 _OPERAND = {_F32: SSD_F32, _BF16: SSD_BF16, _E4M3: SSD_E4M3}
 
 
+# The current device and stream as plain numbers: these calls stand in front of
+# every launch, and the ones that build Stream objects take 2 us.
+_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _arg(t, name, dtype, device, shape):
-    """The address of a contiguous tensor argument (None stays None). The
-    checks stand in one expression; a tensor that fails it goes to _need for
-    its message."""
+    """The address of a contiguous tensor argument on CUDA device number `device`
+    (None stays None). The checks stand in one expression; a tensor that fails it
+    goes to _need for its message."""
     if t is None:
         return None
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device
             and t.shape == shape and t.is_contiguous()):
-        _need(t, name, dtype, device, shape)
+        _need(t, name, dtype, torch.device("cuda", device), shape)
     return t.data_ptr()
 
 
@@ -57,9 +66,9 @@ def _io_code(t, name):
 
 
 def _strided(t, name, dtype, device, shape):
-    """Checks an operand that may be a view with a contiguous last dimension."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != device or t.shape != shape:
-        _need(t.contiguous() if isinstance(t, torch.Tensor) else t, name, dtype, device, shape)
+    """The address of an operand that may be a view with a contiguous last dimension."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device and t.shape == shape):
+        _need(t.contiguous() if isinstance(t, torch.Tensor) else t, name, dtype, torch.device("cuda", device), shape)
     if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
     return t.data_ptr()
@@ -84,11 +93,6 @@ def _row_stride(t, name):
     return stride
 
 
-def _elsewhere(t, stream):
-    """Whether a call on these tensors has to enter their device or `stream`."""
-    return stream is not None or t.device.index != torch.cuda.current_device()
-
-
 class _on:
     """Makes a tensor's device and the stream given for the call the current ones."""
 
@@ -108,10 +112,6 @@ class _on:
             c.__exit__(*exc)
 
 
-def _current(device):
-    return torch.cuda.current_stream(device).cuda_stream
-
-
 def rms_norm(x, weight, residual=None, gate=None, eps: float = 1e-5, groups: int = 1,
              quantize: bool = False, y=None, scale=None, residual_out=None, stream=None):
     """Root-mean-square norm over the last dimension of x [..., D].
@@ -123,10 +123,11 @@ def rms_norm(x, weight, residual=None, gate=None, eps: float = 1e-5, groups: int
     With quantize, y is float8_e4m3fn and scale [...] fp32 holds one factor per
     row: y ~ scale * stored. Returns (y, scale or None, residual_out or None)."""
     code = _io_code(x, "x")
-    if _elsewhere(x, stream):
+    dev = x.get_device()
+    if stream is not None or dev != _device():
         with _on(x, stream):
             return rms_norm(x, weight, residual, gate, eps, groups, quantize, y, scale, residual_out)
-    dev, dtype, shape = x.device, x.dtype, x.shape
+    dtype, shape = x.dtype, x.shape
     if not shape:
         raise ValueError("x must have at least one dimension")
     D = shape[-1]
@@ -156,9 +157,9 @@ def rms_norm(x, weight, residual=None, gate=None, eps: float = 1e-5, groups: int
         gate_stride = _row_stride(gate, "gate")
     if quantize:
         if y is None:
-            y = torch.empty(shape, dtype=_E4M3, device=dev)
+            y = torch.empty_like(x, dtype=_E4M3)
         if scale is None:
-            scale = torch.empty(shape[:-1], dtype=_F32, device=dev)
+            scale = x.new_empty(shape[:-1], dtype=_F32)
         py = _arg(y, "y", _E4M3, dev, shape)
         ps = _arg(scale, "scale", _F32, dev, shape[:-1])
     else:
@@ -169,7 +170,7 @@ def rms_norm(x, weight, residual=None, gate=None, eps: float = 1e-5, groups: int
         py = _arg(y, "y", dtype, dev, shape)
         ps = None
     rc = lib.ssd_rms_norm(px, pr, pg, gate_stride, pw, py, ps, po, rows, D, groups, eps, code,
-                          res_code, SSD_E4M3 if quantize else code, _current(dev))
+                          res_code, SSD_E4M3 if quantize else code, _raw_stream(dev))
     if rc:
         _check(rc, "ssd_rms_norm")
     return y, scale, residual_out
@@ -190,10 +191,11 @@ def linear(x, w, bias=None, activation: str = "none", residual=None, x_scale=Non
     code = _OPERAND.get(x.dtype)
     if code is None:
         raise TypeError(f"x must be float32, bfloat16 or float8_e4m3fn, got {x.dtype}")
-    if _elsewhere(x, stream):
+    dev = x.get_device()
+    if stream is not None or dev != _device():
         with _on(x, stream):
             return linear(x, w, bias, activation, residual, x_scale, w_scale, out_dtype, y)
-    dev, dtype, lead = x.device, x.dtype, x.shape[:-1]
+    dtype, lead = x.dtype, x.shape[:-1]
     if not isinstance(w, torch.Tensor) or w.dim() != 2 or x.dim() < 1:
         raise ValueError("x must be [..., K] and w [N, K]")
     N, K = w.shape
@@ -215,7 +217,7 @@ def linear(x, w, bias=None, activation: str = "none", residual=None, x_scale=Non
         raise TypeError(f"output dtype must be bfloat16 or float32, got {out_dtype}")
     shape = (*lead, N)
     if y is None:
-        y = torch.empty(shape, dtype=out_dtype, device=dev)
+        y = x.new_empty(shape, dtype=out_dtype)
         py = y.data_ptr()
     else:
         py = _arg(y, "y", out_dtype, dev, shape)
@@ -225,7 +227,7 @@ def linear(x, w, bias=None, activation: str = "none", residual=None, x_scale=Non
     rc = lib.ssd_linear(px, x_stride, pw, _arg(x_scale, "x_scale", _F32, dev, lead),
                         _arg(w_scale, "w_scale", _F32, dev, (N,)), _arg(bias, "bias", _F32, dev, (N,)),
                         _arg(residual, "residual", out_dtype, dev, shape), py, M, N, K, act, code,
-                        out_code, _current(dev))
+                        out_code, _raw_stream(dev))
     if rc:
         _check(rc, "ssd_linear")
     return y
@@ -260,11 +262,12 @@ def conv(u, weight, bias, H: int, P: int, G: int, N: int, dt=None, dt_bias=None,
     softplus(dt + dt_bias) or None, final_state or None); final_state, the last
     width - 1 inputs, must not overlap initial_state."""
     code = _io_code(u, "u")
-    if _elsewhere(u, stream):
+    dev = u.get_device()
+    if stream is not None or dev != _device():
         with _on(u, stream):
             return conv(u, weight, bias, H, P, G, N, dt, dt_bias, activation, initial_state,
                         final_state, return_final_state)
-    dev, dtype = u.device, u.dtype
+    dtype = u.dtype
     C = H * P + 2 * G * N
     if u.dim() != 3 or u.shape[2] != C:
         raise ValueError(f"u must be [B, L, {C}], got shape {tuple(u.shape)}")
@@ -272,25 +275,25 @@ def conv(u, weight, bias, H: int, P: int, G: int, N: int, dt=None, dt_bias=None,
     pu = _strided(u, "u", dtype, dev, u.shape)
     W, pw, pb, pdb = _conv_weights(weight, bias, dt, dt_bias, C, H, dev)
     act = _conv_activation(activation)
-    x = torch.empty((B, L, H, P), dtype=dtype, device=dev)
-    Bm = torch.empty((B, L, G, N), dtype=dtype, device=dev)
-    Cm = torch.empty((B, L, G, N), dtype=dtype, device=dev)
+    x = u.new_empty((B, L, H, P))
+    Bm = u.new_empty((B, L, G, N))
+    Cm = torch.empty_like(Bm)
     out = pdt = po = None
     db = dr = 0
     if dt is not None:
         pdt = _strided(dt, "dt", dtype, dev, (B, L, H))
         db, dr, _ = dt.stride()
-        out = torch.empty((B, L, H), dtype=_F32, device=dev)
+        out = u.new_empty((B, L, H), dtype=_F32)
         po = out.data_ptr()
     state_shape = (B, W - 1, C)
     if final_state is None and return_final_state:
-        final_state = torch.empty(state_shape, dtype=dtype, device=dev)
+        final_state = u.new_empty(state_shape)
     ub, ur, _ = u.stride()
     rc = lib.ssd_conv(pu, ub, ur, pw, pb, pdt, db, dr, pdb,
                       _arg(initial_state, "initial_state", dtype, dev, state_shape), x.data_ptr(),
                       Bm.data_ptr(), Cm.data_ptr(), po,
                       _arg(final_state, "final_state", dtype, dev, state_shape), B, L, H, P, G, N, W,
-                      act, code, _current(dev))
+                      act, code, _raw_stream(dev))
     if rc:
         _check(rc, "ssd_conv")
     return x, Bm, Cm, out, final_state
@@ -302,10 +305,11 @@ def conv_step(u, weight, bias, state, H: int, P: int, G: int, N: int, dt=None, d
     dt [B, H] may be views; ``state`` [B, width - 1, C] is shifted in place.
     Returns (x [B, H, P], Bm, Cm [B, G, N], dt' [B, H] fp32 or None)."""
     code = _io_code(u, "u")
-    if _elsewhere(u, stream):
+    dev = u.get_device()
+    if stream is not None or dev != _device():
         with _on(u, stream):
             return conv_step(u, weight, bias, state, H, P, G, N, dt, dt_bias, activation)
-    dev, dtype = u.device, u.dtype
+    dtype = u.dtype
     C = H * P + 2 * G * N
     if u.dim() != 2 or u.shape[1] != C:
         raise ValueError(f"u must be [B, {C}], got shape {tuple(u.shape)}")
@@ -316,18 +320,24 @@ def conv_step(u, weight, bias, state, H: int, P: int, G: int, N: int, dt=None, d
     if state is None:
         raise ValueError("state is required")
     ps = _arg(state, "state", dtype, dev, (B, W - 1, C))
-    x = torch.empty((B, H, P), dtype=dtype, device=dev)
-    Bm = torch.empty((B, G, N), dtype=dtype, device=dev)
-    Cm = torch.empty((B, G, N), dtype=dtype, device=dev)
+    x = u.new_empty((B, H, P))
+    Bm = u.new_empty((B, G, N))
+    Cm = torch.empty_like(Bm)
     out = pdt = po = None
     dr = 0
     if dt is not None:
         pdt = _strided(dt, "dt", dtype, dev, (B, H))
         dr = dt.stride(0)
-        out = torch.empty((B, H), dtype=_F32, device=dev)
+        out = u.new_empty((B, H), dtype=_F32)
         po = out.data_ptr()
     rc = lib.ssd_conv_step(pu, u.stride(0), pw, pb, pdt, dr, pdb, ps, x.data_ptr(), Bm.data_ptr(),
-                           Cm.data_ptr(), po, B, H, P, G, N, W, act, code, _current(dev))
+                           Cm.data_ptr(), po, B, H, P, G, N, W, act, code, _raw_stream(dev))
     if rc:
         _check(rc, "ssd_conv_step")
     return x, Bm, Cm, out
+
+
+def set_linear_variant(variant: int) -> None:
+    """Test hook: 0 automatic, 1 SIMT, 2 the tensor-core kernel for few tokens,
+    3 the one for many (see include/ssd.h)."""
+    lib.ssd_set_linear_variant(int(variant))
