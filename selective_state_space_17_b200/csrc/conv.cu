@@ -77,10 +77,12 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(ConvArgs a, int strip, i
     }
     Packed<float, VEC * W> wt;  // weight of channel j, tap k: element j W + k
     Packed<float, VEC> bias;
-    if constexpr (VEC > 1) wt.load(a.weight + (long long)c * W);
-    else
+    if constexpr (VEC > 1) {
+        wt.load(a.weight + (long long)c * W);
+    } else {
 #pragma unroll
         for (int k = 0; k < W; ++k) wt.w[k] = __float_as_uint(a.weight[(long long)c * W + k]);
+    }
     bias.zero();
     if (a.bias) bias.load(a.bias + c);
     for (int t = t0; t < t1; t += kAhead) {

@@ -69,11 +69,55 @@ void set_linear_variant(int variant);
 
 inline bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
-// v * sigmoid(v). exp of a large negative v's opposite is inf, which divides
-// to 0; the fast exponential and division are off by a few units of 2^-24,
-// below every output's rounding but fp32's, where the sum of both measured
-// 2e-7 of the output.
-__device__ __forceinline__ float silu_f(float v) { return __fdividef(v, 1.0f + __expf(-v)); }
+// v * sigmoid(v) = v / (1 + 2^(-v log2 e)). Where the power overflows, v < -88,
+// the reciprocal of inf is 0 and so is the result. The hardware's approximations
+// of 2^x and 1/x are off by at most 2 and 1 units of 2^-23, below every output's
+// rounding but fp32's, where the whole measured 2e-7 of the output.
+__device__ __forceinline__ float silu_f(float v)
+{
+    float p, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(v * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + p));
+    return v * r;
+}
+
+// Two fp32 lanes in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+__device__ __forceinline__ float2 silu2(float2 v)
+{
+    float2 p = mul2(v, both(-1.4426950408889634f)), r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p.x) : "f"(p.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p.y) : "f"(p.y));
+    p = add2(p, both(1.0f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(p.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(p.y));
+    return mul2(v, r);
+}
 
 __device__ __forceinline__ float gelu_f(float v)
 {
@@ -138,6 +182,12 @@ struct Packed {
     {
         if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
         else return __uint_as_float((i & 1) ? (w[i / 2] & 0xFFFF0000u) : (w[i / 2] << 16));
+    }
+    // elements 2i and 2i + 1 (0 beside a single one)
+    __device__ __forceinline__ float2 pair(int i) const
+    {
+        if constexpr (VEC == 1) return make_float2(get(0), 0.0f);
+        else return make_float2(get(2 * i), get(2 * i + 1));
     }
     __device__ __forceinline__ void set(const float* v)
     {

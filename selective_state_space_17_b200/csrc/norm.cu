@@ -29,14 +29,31 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return r;
 }
 
+// max(a, |b.x|, |b.y|), NaN if one of them is.
+__device__ __forceinline__ float max_abs(float a, float2 b)
+{
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b.x), "f"(b.y));
+    return r;
+}
+
+// The warp's maximum, NaN if one of its values is.
+__device__ __forceinline__ float warp_max(float v)
+{
+    float r;
+    asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// The warp's sum of v.x, and with MAX its maximum of v.y.
+template <bool MAX>
 __device__ __forceinline__ float2 warp_sum_max(float2 v)
 {
+    float2 r = v;
+    if constexpr (MAX) r.y = warp_max(v.y);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-        v.y = max_nan(v.y, __shfl_xor_sync(0xffffffffu, v.y, o));
-    }
-    return v;
+    for (int o = 16; o; o >>= 1) r.x += __shfl_xor_sync(0xffffffffu, r.x, o);
+    return r;
 }
 
 template <int VEC>
@@ -60,158 +77,266 @@ __device__ __forceinline__ void store_e4m3(uint8_t* p, const float* v)
 }
 
 // A row is spread over `groups` x `wpg` warps, whole warps to one group, and
-// each lane takes vectors of VEC elements, wpg * 32 vectors apart. With VPT > 0
-// a lane has at most VPT of them and keeps them in registers; VPT = 0 takes any
-// width and reads the row a second time for the output. When a row fits one
-// warp a CTA runs blockDim / 32 rows at a time and needs no barrier.
+// each lane takes vectors of VEC elements, wpg * 32 vectors apart. When a row
+// fits one warp a CTA runs blockDim / 32 rows at a time and needs no barrier.
+struct Place {
+    int lane, warp, wpr, wr, group, t0, stride, nvec, Dg;
+    long long gbase;
+    __device__ __forceinline__ Place(const NormArgs& a, int wpg, int vec)
+    {
+        lane = threadIdx.x & 31;
+        warp = threadIdx.x >> 5;
+        wpr = a.groups * wpg;
+        wr = wpr == 1 ? 0 : warp;
+        group = wr / wpg;
+        Dg = a.D / a.groups;
+        nvec = Dg / vec;
+        stride = wpg * 32;
+        t0 = (wr - group * wpg) * 32 + lane;
+        gbase = (long long)group * Dg;
+    }
+    __device__ __forceinline__ long long row0() const
+    {
+        return wpr == 1 ? (long long)blockIdx.x * (blockDim.x >> 5) + warp : blockIdx.x;
+    }
+    __device__ __forceinline__ long long row_step() const
+    {
+        return (long long)gridDim.x * (wpr == 1 ? blockDim.x >> 5 : 1);
+    }
+};
+
+// Factors from v w to the output: v w * first * second.
+struct Factors {
+    float first, second;
+};
+
+// Joins the lanes' (sum of squares, max |v w|) of a row: returns rho of this
+// thread's group, with Q8 over the row's scale s, which it stores. In one
+// factor, rho / s, but for rows so small that it overflows (a row of zeros).
+// red alternates between two buffers: a warp writes the next row's only after
+// this row's barrier, which follows every read of the one before.
+template <bool Q8>
+__device__ __forceinline__ Factors join_row(float2 acc, const NormArgs& a, const Place& p, int wpg, float2* red,
+                                          long long row)
+{
+    acc = warp_sum_max<Q8>(acc);
+    float amax = 0.0f;  // max |y|
+    const float n = (float)p.Dg;
+    if (p.wpr > 1) {
+        if (p.lane == 0) red[p.warp] = acc;
+        __syncthreads();
+        if (a.groups == 1) {
+            acc = make_float2(0.0f, 0.0f);
+#pragma unroll 4
+            for (int k = 0; k < p.wpr; ++k) {
+                acc.x += red[k].x;
+                acc.y = max_nan(acc.y, red[k].y);
+            }
+            if constexpr (Q8) amax = acc.y * rsqrtf(acc.x / n + a.eps);
+        } else {
+            // lane g joins group g; its share of the maximum is rho_g max |v w|
+            float2 t = make_float2(0.0f, 0.0f);
+            if (p.lane < a.groups) {
+                for (int k = 0; k < wpg; ++k) {
+                    const float2 e = red[p.lane * wpg + k];
+                    t.x += e.x;
+                    t.y = max_nan(t.y, e.y);
+                }
+                if constexpr (Q8) t.y *= rsqrtf(t.x / n + a.eps);
+            }
+            acc.x = __shfl_sync(0xffffffffu, t.x, p.group);
+            if constexpr (Q8) amax = warp_max(t.y);
+        }
+    } else if constexpr (Q8) {
+        amax = acc.y * rsqrtf(acc.x / n + a.eps);
+    }
+    const float rho = rsqrtf(acc.x / n + a.eps);
+    if constexpr (!Q8) return {rho, 1.0f};
+    const float s = max_nan(amax / kE4m3Max, kScaleMin);
+    if (p.wr == 0 && p.lane == 0) a.scale[row] = s;
+    const float f = rho / s;
+    if (isinf(f)) return {rho, 1.0f / s};
+    return {f, 1.0f};
+}
+
+// v of one vector: x + r, x silu(z) or x.
+template <typename T, typename R, int MODE, int VEC>
+struct Operands {
+    Packed<T, VEC> x, z;
+    Packed<R, VEC> r;
+    __device__ __forceinline__ void load(const NormArgs& a, long long at, long long zat)
+    {
+        x.load(static_cast<const T*>(a.x) + at);
+        if constexpr (MODE == kGate) z.load(static_cast<const T*>(a.gate) + zat);
+        if constexpr (MODE == kResidual) r.load(static_cast<const R*>(a.residual) + at);
+    }
+    __device__ __forceinline__ float2 pair(int i) const
+    {
+        float2 v = x.pair(i);
+        if constexpr (MODE == kResidual) v = add2(v, r.pair(i));
+        if constexpr (MODE == kGate) v = mul2(v, silu2(z.pair(i)));
+        return v;
+    }
+};
+
+template <typename T, bool Q8, int VEC>
+__device__ __forceinline__ void store_out(const NormArgs& a, long long at, const float* o)
+{
+    if constexpr (Q8) {
+        store_e4m3<VEC>(static_cast<uint8_t*>(a.y) + at, o);
+    } else {
+        Packed<T, VEC> p;
+        p.set(o);
+        p.store(static_cast<T*>(a.y) + at);
+    }
+}
+
+template <typename R, int VEC>
+__device__ __forceinline__ void store_residual(const NormArgs& a, long long at, const float* v)
+{
+    if (a.residual_out) {
+        Packed<R, VEC> p;
+        p.set(v);
+        p.store(static_cast<R*>(a.residual_out) + at);
+    }
+}
+
+// Whether a lane keeps its weights in shared memory (see below): with the gate
+// the arithmetic wants the warps that 64 registers a thread allow (16384 x 5120
+// to 8 bits 234 us with two CTAs per SM, 127 with three); with a residual the
+// loads in flight alone count and registers are faster (16384 x 2560 74 to 80 us).
+__host__ __device__ constexpr bool shared_weights(int mode, int values) { return values > 8 && mode != kResidual; }
+
+// Rows kept in registers, VPT vectors to a lane. A CTA walks rows a grid apart
+// with the next row's loads in flight under the
+// reduction and the output of the row at hand. v w replaces v as soon as its
+// square is added, so the output costs one product and the weights are not read
+// again.
 template <typename T, typename R, int MODE, bool Q8, int VEC, int VPT>
-__global__ void __launch_bounds__(1024)
-rms_norm_kernel(NormArgs a, int wpg)
+__global__ void __launch_bounds__(VPT * VEC > 8 ? 512 : 1024, shared_weights(MODE, VPT * VEC) ? 2 : 1) rms_norm_kernel(NormArgs a, int wpg)
 {
     __shared__ float2 red[2][32];
-    constexpr bool kKeep = VPT > 0;
-    constexpr int kV = kKeep ? VPT : 1;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int wpr = a.groups * wpg;               // warps of a row
-    const int rows_per_cta = wpr == 1 ? (int)(blockDim.x >> 5) : 1;
-    const int wr = wpr == 1 ? 0 : warp;           // this warp within its row
-    const int group = wr / wpg;
-    const int Dg = a.D / a.groups;
-    const int nvec = Dg / VEC;                    // vectors of a group
-    const int t0 = (wr - group * wpg) * 32 + lane, stride = wpg * 32;
-    const long long gbase = (long long)group * Dg;
-    const T* x = static_cast<const T*>(a.x);
-    const R* res = static_cast<const R*>(a.residual);
-    const T* gate = static_cast<const T*>(a.gate);
-    R* res_out = static_cast<R*>(a.residual_out);
-    int buf = 0;
-
-    // sum of squares and max |v w| of one vector; v into val, v w into vw
-    auto combine = [&](const Packed<T, VEC>& px, const Packed<T, VEC>& pz, const Packed<R, VEC>& pr,
-                       float* val) {
+    extern __shared__ float4 weights[];
+    const Place p(a, wpg, VEC);
+    Operands<T, R, MODE, VEC> in[VPT];
+    // each thread's own weights: in registers, or, where its vectors would take
+    // more than a quarter of them, in its own places in shared memory (read 16
+    // bytes at a time by neighbouring lanes: no conflicts, no barrier)
+    constexpr bool kShared = shared_weights(MODE, VPT * VEC);
+    constexpr int kPairs = (VEC + 1) / 2;
+    Packed<float, VEC> w[VPT];
+    long long row = p.row0();
+    if (row >= a.rows) return;
+    auto load = [&](long long r) {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            float v = px.get(j);
-            if constexpr (MODE == kResidual) v += pr.get(j);
-            if constexpr (MODE == kGate) v *= silu_f(pz.get(j));
-            val[j] = v;
+        for (int i = 0; i < VPT; ++i) {
+            const int t = p.t0 + i * p.stride;
+            if (t < p.nvec) in[i].load(a, r * a.D + p.gbase + t * VEC, r * a.gate_stride + p.gbase + t * VEC);
         }
     };
+    load(row);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        w[i].zero();
+        if (p.t0 + i * p.stride < p.nvec) w[i].load(a.weight + p.gbase + (p.t0 + i * p.stride) * VEC);
+        if constexpr (kShared) {
+#pragma unroll
+            for (int j = 0; j < VEC / 4; ++j)
+                weights[(i * (VEC / 4) + j) * blockDim.x + threadIdx.x] =
+                    make_float4(w[i].get(4 * j), w[i].get(4 * j + 1), w[i].get(4 * j + 2), w[i].get(4 * j + 3));
+        }
+    }
+    for (int buf = 0; row < a.rows; buf ^= 1) {
+        const long long base = row * a.D + p.gbase, next = row + p.row_step();
+        float2 vw[VPT][kPairs];
+        float2 squares = both(0.0f);
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int t = p.t0 + i * p.stride;
+            if (t >= p.nvec) break;
+            Packed<float, VEC> wv = w[i];
+            if constexpr (kShared) {
+#pragma unroll
+                for (int j = 0; j < VEC / 4; ++j) {
+                    const float4 q = weights[(i * (VEC / 4) + j) * blockDim.x + threadIdx.x];
+                    wv.w[4 * j] = __float_as_uint(q.x); wv.w[4 * j + 1] = __float_as_uint(q.y);
+                    wv.w[4 * j + 2] = __float_as_uint(q.z); wv.w[4 * j + 3] = __float_as_uint(q.w);
+                }
+            }
+            float v[2 * kPairs];
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) {
+                const float2 e = in[i].pair(j);
+                squares = fma2(e, e, squares);
+                vw[i][j] = mul2(e, wv.pair(j));
+                if constexpr (Q8) top = max_abs(top, vw[i][j]);
+                v[2 * j] = e.x; v[2 * j + 1] = e.y;
+            }
+            if constexpr (MODE == kResidual) store_residual<R, VEC>(a, base + t * VEC, v);
+        }
+        if (next < a.rows) load(next);
+        const Factors f = join_row<Q8>(make_float2(squares.x + squares.y, top), a, p, wpg, red[buf], row);
+        if (Q8 && f.second != 1.0f) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+#pragma unroll
+                for (int j = 0; j < kPairs; ++j) vw[i][j] = mul2(vw[i][j], both(f.second));
+        }
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int t = p.t0 + i * p.stride;
+            if (t >= p.nvec) break;
+            float o[2 * kPairs];
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) {
+                const float2 e = mul2(vw[i][j], both(f.first));
+                o[2 * j] = e.x; o[2 * j + 1] = e.y;
+            }
+            store_out<T, Q8, VEC>(a, base + t * VEC, o);
+        }
+        row = next;
+    }
+}
 
-    for (long long row = (long long)blockIdx.x * rows_per_cta + (wpr == 1 ? warp : 0); row < a.rows;
-         row += (long long)gridDim.x * rows_per_cta) {
-        const long long base = row * a.D + gbase;
-        const long long zbase = row * a.gate_stride + gbase;
-        float val[kV][VEC];
-        float2 acc = make_float2(0.0f, 0.0f);
-        const int iters = kKeep ? kV : (nvec + stride - 1 - t0) / stride;
-        auto load_combine = [&](int i, float* v) {
-            const long long c = (long long)(t0 + i * stride) * VEC;
-            Packed<T, VEC> px, pz;
-            Packed<R, VEC> pr;
-            px.load(x + base + c);
-            if constexpr (MODE == kGate) pz.load(gate + zbase + c);
-            if constexpr (MODE == kResidual) pr.load(res + base + c);
-            combine(px, pz, pr, v);
-        };
-        if constexpr (kKeep) {
-            Packed<T, VEC> px[kV], pz[kV];
-            Packed<R, VEC> pr[kV];
+// Rows of any width, read a second time for the output.
+template <typename T, typename R, int MODE, bool Q8, int VEC>
+__global__ void __launch_bounds__(1024) rms_norm_wide_kernel(NormArgs a, int wpg)
+{
+    __shared__ float2 red[2][32];
+    constexpr int kPairs = (VEC + 1) / 2;
+    const Place p(a, wpg, VEC);
+    int buf = 0;
+    for (long long row = p.row0(); row < a.rows; row += p.row_step(), buf ^= 1) {
+        const long long base = row * a.D + p.gbase, zbase = row * a.gate_stride + p.gbase;
+        Operands<T, R, MODE, VEC> in;
+        Packed<float, VEC> w;
+        float2 squares = both(0.0f);
+        float top = 0.0f;
+        for (int t = p.t0; t < p.nvec; t += p.stride) {
+            in.load(a, base + t * VEC, zbase + t * VEC);
+            if constexpr (Q8) w.load(a.weight + p.gbase + t * VEC);
 #pragma unroll
-            for (int i = 0; i < kV; ++i) {
-                px[i].zero(); pz[i].zero(); pr[i].zero();
-                if (t0 + i * stride < nvec) {
-                    const long long c = (long long)(t0 + i * stride) * VEC;
-                    px[i].load(x + base + c);
-                    if constexpr (MODE == kGate) pz[i].load(gate + zbase + c);
-                    if constexpr (MODE == kResidual) pr[i].load(res + base + c);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kV; ++i) combine(px[i], pz[i], pr[i], val[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < iters; ++i) {
-            if (t0 + i * stride >= nvec) break;
-            float* v = val[kKeep ? i : 0];
-            if constexpr (!kKeep) load_combine(i, v);
-            float wv[VEC];
-            if constexpr (Q8) {
-                Packed<float, VEC> pw;
-                pw.load(a.weight + gbase + (long long)(t0 + i * stride) * VEC);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) wv[j] = pw.get(j);
-            }
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                acc.x = fmaf(v[j], v[j], acc.x);
-                if constexpr (Q8) acc.y = max_nan(acc.y, fabsf(v[j] * wv[j]));
+            for (int j = 0; j < kPairs; ++j) {
+                const float2 v = in.pair(j);
+                squares = fma2(v, v, squares);
+                if constexpr (Q8) top = max_abs(top, mul2(v, w.pair(j)));
             }
         }
-        acc = warp_sum_max(acc);
-        float amax_y = 0.0f;
-        if (wpr > 1) {
-            // two buffers: a warp writes the next row's only after this row's
-            // barrier, which follows every read of the buffer before it
-            if (lane == 0) red[buf][warp] = acc;
-            __syncthreads();
-            float sum = 0.0f;
-            if (a.groups == 1) {
-                acc = warp_sum_max(lane < wpr ? red[buf][lane] : make_float2(0.0f, 0.0f));
-                sum = acc.x;
-                if constexpr (Q8) amax_y = acc.y * rsqrtf(sum / (float)Dg + a.eps);
-            } else {
-                for (int g = 0; g < a.groups; ++g) {
-                    float2 t = make_float2(0.0f, 0.0f);
-                    for (int k = 0; k < wpg; ++k) {
-                        const float2 e = red[buf][g * wpg + k];
-                        t.x += e.x;
-                        t.y = max_nan(t.y, e.y);
-                    }
-                    if (g == group) sum = t.x;
-                    if constexpr (Q8) amax_y = max_nan(amax_y, t.y * rsqrtf(t.x / (float)Dg + a.eps));
-                }
-            }
-            acc.x = sum;
-            buf ^= 1;
-        } else if constexpr (Q8) {
-            amax_y = acc.y * rsqrtf(acc.x / (float)Dg + a.eps);
-        }
-        const float rho = rsqrtf(acc.x / (float)Dg + a.eps);
-        float inv = 1.0f;
-        if constexpr (Q8) {
-            const float s = max_nan(amax_y / kE4m3Max, kScaleMin);
-            if (wr == 0 && lane == 0) a.scale[row] = s;
-            inv = 1.0f / s;
-        }
+        const Factors f = join_row<Q8>(make_float2(squares.x + squares.y, top), a, p, wpg, red[buf], row);
+        for (int t = p.t0; t < p.nvec; t += p.stride) {
+            in.load(a, base + t * VEC, zbase + t * VEC);
+            w.load(a.weight + p.gbase + t * VEC);
+            float v[2 * kPairs], o[2 * kPairs];
 #pragma unroll
-        for (int i = 0; i < iters; ++i) {
-            if (t0 + i * stride >= nvec) break;
-            const long long c = (long long)(t0 + i * stride) * VEC;
-            float* v = val[kKeep ? i : 0];
-            if constexpr (!kKeep) load_combine(i, v);
-            if constexpr (MODE == kResidual) {
-                if (res_out) {
-                    Packed<R, VEC> po;
-                    po.set(v);
-                    po.store(res_out + base + c);
-                }
+            for (int j = 0; j < kPairs; ++j) {
+                const float2 e = in.pair(j);
+                const float2 q = mul2(mul2(mul2(e, w.pair(j)), both(f.first)), both(f.second));
+                v[2 * j] = e.x; v[2 * j + 1] = e.y;
+                o[2 * j] = q.x; o[2 * j + 1] = q.y;
             }
-            Packed<float, VEC> pw;
-            pw.load(a.weight + gbase + c);
-            float o[VEC];
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                o[j] = v[j] * pw.get(j) * rho;
-                if constexpr (Q8) o[j] *= inv;
-            }
-            if constexpr (Q8) {
-                store_e4m3<VEC>(static_cast<uint8_t*>(a.y) + base + c, o);
-            } else {
-                Packed<T, VEC> po;
-                po.set(o);
-                po.store(static_cast<T*>(a.y) + base + c);
-            }
+            if constexpr (MODE == kResidual) store_residual<R, VEC>(a, base + t * VEC, v);
+            store_out<T, Q8, VEC>(a, base + t * VEC, o);
         }
     }
 }
@@ -220,20 +345,22 @@ template <typename T, typename R, int MODE, bool Q8, int VEC, int VPT>
 cudaError_t launch(const NormArgs& a, const LaunchCtx& ctx)
 {
     const int nvec = a.D / a.groups / VEC;
-    const int most = 32 / a.groups;  // warps a group may have
-    int wpg = VPT ? (nvec + 32 * VPT - 1) / (32 * VPT) : std::min(most, (nvec + 31) / 32);
-    wpg = std::max(1, std::min(wpg, most));
+    int wpg;
+    if constexpr (VPT > 0) wpg = (nvec + 32 * VPT - 1) / (32 * VPT);
+    else wpg = std::min(32 / a.groups, (nvec + 31) / 32);
     const int wpr = wpg * a.groups;
     const int threads = wpr == 1 ? 128 : wpr * 32;
     const long long ctas = wpr == 1 ? (a.rows + 3) / 4 : a.rows;
-    const long long cap = (long long)ctx.num_sms * std::max(1, 2048 / threads);
-    rms_norm_kernel<T, R, MODE, Q8, VEC, VPT>
-        <<<(unsigned)std::min(ctas, cap), threads, 0, ctx.stream>>>(a, wpg);
+    const long long cap = (long long)ctx.num_sms * std::max(1, 1024 / threads);
+    const unsigned grid = (unsigned)std::min(ctas, cap);
+    const size_t smem = shared_weights(MODE, VPT * VEC) ? sizeof(float) * VPT * VEC * threads : 0;
+    if constexpr (VPT > 0) rms_norm_kernel<T, R, MODE, Q8, VEC, VPT><<<grid, threads, smem, ctx.stream>>>(a, wpg);
+    else rms_norm_wide_kernel<T, R, MODE, Q8, VEC><<<grid, threads, 0, ctx.stream>>>(a, wpg);
     return cudaGetLastError();
 }
 
 // The widest access that every row allows (16 bytes of the I/O dtype), and the
-// fewest vectors per lane that put a group in registers.
+// vectors per lane that put a row in the registers of one CTA.
 template <typename T, typename R, int MODE, bool Q8>
 cudaError_t pick(const NormArgs& a, const LaunchCtx& ctx)
 {
@@ -241,14 +368,17 @@ cudaError_t pick(const NormArgs& a, const LaunchCtx& ctx)
     const int Dg = a.D / a.groups;
     const bool vec = Dg % V == 0 &&
                      (MODE != kGate || (aligned_to(a.gate, 16) && a.gate_stride % V == 0));
-    const int lanes = 32 * (32 / a.groups);  // lanes a group may have in a CTA of 1024
-    const int n = vec ? Dg / V : Dg;
+    // whether n vectors of a group, k to a lane, fit `warps` warps shared by the groups
+    auto fits = [&](int n, int k, int warps) { return (n + 32 * k - 1) / (32 * k) * a.groups <= warps; };
     if (vec) {
-        if (n <= lanes) return launch<T, R, MODE, Q8, V, 1>(a, ctx);
-        if (n <= 2 * lanes) return launch<T, R, MODE, Q8, V, 2>(a, ctx);
+        const int n = Dg / V;
+        const bool many = a.rows > 4ll * ctx.num_sms;
+        if (fits(n, 1, many ? 1 : 32)) return launch<T, R, MODE, Q8, V, 1>(a, ctx);
+        if (fits(n, 2, 16)) return launch<T, R, MODE, Q8, V, 2>(a, ctx);
+        if (fits(n, 1, 32)) return launch<T, R, MODE, Q8, V, 1>(a, ctx);
         return launch<T, R, MODE, Q8, V, 0>(a, ctx);
     }
-    if (n <= 4 * lanes) return launch<T, R, MODE, Q8, 1, 4>(a, ctx);
+    if (fits(Dg, 4, 32)) return launch<T, R, MODE, Q8, 1, 4>(a, ctx);
     return launch<T, R, MODE, Q8, 1, 0>(a, ctx);
 }
 
