@@ -67,6 +67,10 @@ cudaError_t linear(const LinearArgs& a, const LaunchCtx& ctx);       // the tens
 cudaError_t linear_simt(const LinearArgs& a, const LaunchCtx& ctx);  // any operands
 void set_linear_variant(int variant);
 
+// Lets a kernel take up to `bytes` of dynamic shared memory on the current
+// device; asks the runtime once per kernel, device and size (layer_api.cu).
+cudaError_t allow_smem(const void* kernel, int bytes);
+
 inline bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
 // v * sigmoid(v) = v / (1 + 2^(-v log2 e)). Where the power overflows, v < -88,

@@ -243,7 +243,7 @@ cudaError_t launch_few(const LinearArgs& a, const Epilogue& e, int splits, const
         !make_map_rows(&xmap, a.x, E4M3, a.K, a.M, (uint64_t)a.x_stride * es, BN))
         return cudaErrorInvalidValue;
     auto* kernel = linear_few_kernel<BN, E4M3, O>;
-    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem);
+    cudaError_t err = allow_smem(reinterpret_cast<const void*>(kernel), F::kSmem);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(splits, tn, tm);
@@ -607,7 +607,7 @@ cudaError_t launch_many(const LinearArgs& a, const Epilogue& e, const LaunchCtx&
         return cudaErrorInvalidValue;
     const bool wide = (long long)a.N * sizeof(O) % 32 == 0 && aligned_to(a.y, 32) && aligned_to(a.residual, 32);
     auto* kernel = wide ? linear_many_kernel<BN, E4M3, O, SEG, true> : linear_many_kernel<BN, E4M3, O, SEG, false>;
-    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
+    cudaError_t err = allow_smem(reinterpret_cast<const void*>(kernel), T::kSmem);
     if (err != cudaSuccess) return err;
     const int pairs = (int)std::min<long long>(t.all, ctx.num_sms / 2);
     kernel<<<2 * pairs, T::kThreads, T::kSmem, ctx.stream>>>(wmap, xmap, e, t, kblocks, ctx.status);

@@ -121,40 +121,45 @@ __device__ __forceinline__ Factors join_row(float2 acc, const NormArgs& a, const
 {
     acc = warp_sum_max<Q8>(acc);
     float amax = 0.0f;  // max |y|
-    const float n = (float)p.Dg;
+    const float inv_n = 1.0f / (float)p.Dg;
     if (p.wpr > 1) {
         if (p.lane == 0) red[p.warp] = acc;
         __syncthreads();
         if (a.groups == 1) {
-            acc = make_float2(0.0f, 0.0f);
-#pragma unroll 4
-            for (int k = 0; k < p.wpr; ++k) {
-                acc.x += red[k].x;
-                acc.y = max_nan(acc.y, red[k].y);
+            if (p.wpr <= 16) {
+                // both halves of the warp join the same sixteen
+                const int k = p.lane & 15;
+                const float2 e = k < p.wpr ? red[k] : both(0.0f);
+                acc.x = e.x;
+#pragma unroll
+                for (int o = 8; o; o >>= 1) acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o);
+                if constexpr (Q8) acc.y = warp_max(e.y);
+            } else {
+                acc = warp_sum_max<Q8>(p.lane < p.wpr ? red[p.lane] : both(0.0f));
             }
-            if constexpr (Q8) amax = acc.y * rsqrtf(acc.x / n + a.eps);
+            if constexpr (Q8) amax = acc.y * rsqrtf(fmaf(acc.x, inv_n, a.eps));
         } else {
             // lane g joins group g; its share of the maximum is rho_g max |v w|
-            float2 t = make_float2(0.0f, 0.0f);
+            float2 t = both(0.0f);
             if (p.lane < a.groups) {
                 for (int k = 0; k < wpg; ++k) {
                     const float2 e = red[p.lane * wpg + k];
                     t.x += e.x;
                     t.y = max_nan(t.y, e.y);
                 }
-                if constexpr (Q8) t.y *= rsqrtf(t.x / n + a.eps);
+                if constexpr (Q8) t.y *= rsqrtf(fmaf(t.x, inv_n, a.eps));
             }
             acc.x = __shfl_sync(0xffffffffu, t.x, p.group);
             if constexpr (Q8) amax = warp_max(t.y);
         }
     } else if constexpr (Q8) {
-        amax = acc.y * rsqrtf(acc.x / n + a.eps);
+        amax = acc.y * rsqrtf(fmaf(acc.x, inv_n, a.eps));
     }
-    const float rho = rsqrtf(acc.x / n + a.eps);
+    const float rho = rsqrtf(fmaf(acc.x, inv_n, a.eps));
     if constexpr (!Q8) return {rho, 1.0f};
-    const float s = max_nan(amax / kE4m3Max, kScaleMin);
+    const float s = max_nan(amax * (1.0f / kE4m3Max), kScaleMin);
     if (p.wr == 0 && p.lane == 0) a.scale[row] = s;
-    const float f = rho / s;
+    const float f = __fdividef(rho, s);
     if (isinf(f)) return {rho, 1.0f / s};
     return {f, 1.0f};
 }
@@ -169,6 +174,12 @@ struct Operands {
         x.load(static_cast<const T*>(a.x) + at);
         if constexpr (MODE == kGate) z.load(static_cast<const T*>(a.gate) + zat);
         if constexpr (MODE == kResidual) r.load(static_cast<const R*>(a.residual) + at);
+    }
+    __device__ __forceinline__ void zero()
+    {
+        x.zero();
+        z.zero();
+        r.zero();
     }
     __device__ __forceinline__ float2 pair(int i) const
     {
@@ -234,9 +245,11 @@ __global__ void __launch_bounds__(VPT * VEC > 8 ? 512 : 1024, shared_weights(MOD
             if (t < p.nvec) in[i].load(a, r * a.D + p.gbase + t * VEC, r * a.gate_stride + p.gbase + t * VEC);
         }
     };
-    load(row);
+    // a lane's vectors past the row's end hold zeros, which change neither the
+    // sum nor the maximum: only loads and stores ask
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
+        in[i].zero();
         w[i].zero();
         if (p.t0 + i * p.stride < p.nvec) w[i].load(a.weight + p.gbase + (p.t0 + i * p.stride) * VEC);
         if constexpr (kShared) {
@@ -246,6 +259,7 @@ __global__ void __launch_bounds__(VPT * VEC > 8 ? 512 : 1024, shared_weights(MOD
                     make_float4(w[i].get(4 * j), w[i].get(4 * j + 1), w[i].get(4 * j + 2), w[i].get(4 * j + 3));
         }
     }
+    load(row);
     for (int buf = 0; row < a.rows; buf ^= 1) {
         const long long base = row * a.D + p.gbase, next = row + p.row_step();
         float2 vw[VPT][kPairs];
@@ -254,7 +268,6 @@ __global__ void __launch_bounds__(VPT * VEC > 8 ? 512 : 1024, shared_weights(MOD
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int t = p.t0 + i * p.stride;
-            if (t >= p.nvec) break;
             Packed<float, VEC> wv = w[i];
             if constexpr (kShared) {
 #pragma unroll
@@ -273,7 +286,9 @@ __global__ void __launch_bounds__(VPT * VEC > 8 ? 512 : 1024, shared_weights(MOD
                 if constexpr (Q8) top = max_abs(top, vw[i][j]);
                 v[2 * j] = e.x; v[2 * j + 1] = e.y;
             }
-            if constexpr (MODE == kResidual) store_residual<R, VEC>(a, base + t * VEC, v);
+            if constexpr (MODE == kResidual) {
+                if (t < p.nvec) store_residual<R, VEC>(a, base + t * VEC, v);
+            }
         }
         if (next < a.rows) load(next);
         const Factors f = join_row<Q8>(make_float2(squares.x + squares.y, top), a, p, wpg, red[buf], row);
@@ -286,14 +301,13 @@ __global__ void __launch_bounds__(VPT * VEC > 8 ? 512 : 1024, shared_weights(MOD
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int t = p.t0 + i * p.stride;
-            if (t >= p.nvec) break;
             float o[2 * kPairs];
 #pragma unroll
             for (int j = 0; j < kPairs; ++j) {
                 const float2 e = mul2(vw[i][j], both(f.first));
                 o[2 * j] = e.x; o[2 * j + 1] = e.y;
             }
-            store_out<T, Q8, VEC>(a, base + t * VEC, o);
+            if (t < p.nvec) store_out<T, Q8, VEC>(a, base + t * VEC, o);
         }
         row = next;
     }
