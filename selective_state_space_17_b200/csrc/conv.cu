@@ -6,12 +6,17 @@
 //
 // with the W - 1 tokens before token 0 taken from a state (zeros without one).
 // Bound by HBM: each input element is read once and each output written once.
-// A thread walks a strip of tokens of VEC neighbouring channels (one 16-byte
-// access per token) with the window's W - 1 older inputs and the channels'
-// W weights in registers, so a strip reads its tokens and W - 1 more; strips of
-// one channel lie in one CTA column and their overlap hits L2. The single-token
-// form is the same kernel with one token per strip; it loads its whole window
-// at once and may write the state in place.
+// A thread walks a strip of tokens of VEC neighbouring channels with the
+// window's inputs and the channels' W weights in registers and the next tokens'
+// loads in flight, so a strip reads its tokens and W - 1 more; neighbouring
+// strips run at about the same time, and their overlap hits L2. What counts is the
+// bytes in flight: four channels to a thread (8 bytes of bf16) and each token's
+// load eight tokens before its use measured 71.5 us at 4 x 4096 x 5376 in bf16,
+// 5.0 TB/s, four tokens ahead 82 us, and eight channels with four tokens loaded
+// before each four 118 us at 127 registers a thread. The exponentials and
+// reciprocals of SiLU take 40 us of the special-function unit meanwhile. The
+// single-token form is the same kernel with one token per strip; it may shift the
+// state in place.
 #include <algorithm>
 
 #include "layer.cuh"
@@ -20,7 +25,6 @@ namespace ssd {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kAhead = 4;  // tokens loaded before the first of them is used
 
 __device__ __forceinline__ float softplus_f(float v)
 {
@@ -28,22 +32,24 @@ __device__ __forceinline__ float softplus_f(float v)
     return fmaxf(v, 0.0f) + log1pf(expf(-fabsf(v)));
 }
 
-template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(kThreads) conv_kernel(ConvArgs a, int strip, int channel_ctas)
+// kAhead: tokens whose loads are in flight. The launch bound holds bf16 at 72
+// registers a thread, seven CTAs per SM (71.5 us against 73.6 at 80 registers).
+template <typename T, int VEC, int W, int kAhead>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && VEC > 1 && kAhead > 1 ? 7 : 1) conv_kernel(ConvArgs a, int strip, int channel_ctas)
 {
     const int b = blockIdx.z;
     const int t0 = blockIdx.y * strip, t1 = min(t0 + strip, a.L);
     if ((int)blockIdx.x >= channel_ctas) {
         // step sizes of this strip's tokens
         const T* raw = static_cast<const T*>(a.dt_raw) + b * a.dt_batch;
-        const long long n = (long long)(t1 - t0) * a.H;
-        const int step = ((int)gridDim.x - channel_ctas) * kThreads;
-        for (long long i = ((int)blockIdx.x - channel_ctas) * kThreads + threadIdx.x; i < n; i += step) {
-            const int t = t0 + (int)(i / a.H), h = (int)(i % a.H);
-            float v = io<T>::load(raw + t * a.dt_row + h);
-            if (a.dt_bias) v += __ldg(a.dt_bias + h);
-            a.dt[((long long)b * a.L + t) * a.H + h] = softplus_f(v);
-        }
+        // a warp to a token, its lanes along the heads
+        const int warps = ((int)gridDim.x - channel_ctas) * (kThreads / 32);
+        for (int t = t0 + (((int)blockIdx.x - channel_ctas) * kThreads + threadIdx.x) / 32; t < t1; t += warps)
+            for (int h = threadIdx.x & 31; h < a.H; h += 32) {
+                float v = io<T>::load(raw + t * a.dt_row + h);
+                if (a.dt_bias) v += __ldg(a.dt_bias + h);
+                a.dt[((long long)b * a.L + t) * a.H + h] = softplus_f(v);
+            }
         return;
     }
     const int C = a.C();
@@ -51,7 +57,7 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(ConvArgs a, int strip, i
     if (c >= C) return;
     const T* u = static_cast<const T*>(a.u) + b * a.u_batch + c;
     const T* init = static_cast<const T*>(a.init) + (long long)b * (W - 1) * C + c;
-    // the output section of these channels (sections are multiples of VEC)
+    // the output section of these channels (a section is a multiple of VEC)
     T* out;
     int width;
     if (c < a.XC) {
@@ -66,96 +72,123 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(ConvArgs a, int strip, i
     }
     out += ((long long)b * a.L + t0) * width;
 
-    // the window: win[k] is input t - (W - 1) + k of the token t at hand
-    Packed<T, VEC> win[W - 1 + kAhead];
+    constexpr int kPairs = (VEC + 1) / 2;
+    // input t of these channels, or of the state before token 0
+    auto input = [&](int t, Packed<T, VEC>& p) {
+        p.zero();
+        if (t >= 0) p.load(u + t * a.u_row);
+        else if (a.init) p.load(init + (long long)(t + W - 1) * C);
+    };
+    // the window: win[k] is input t - (W - 1) + k of the token t at hand, in
+    // fp32; next holds that token and those after it as they were read
+    float2 win[W][kPairs];
+    Packed<T, VEC> next[kAhead], before[W - 1];
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) {
-        const int t = t0 - (W - 1) + k;
-        win[k].zero();
-        if (t >= 0) win[k].load(u + t * a.u_row);
-        else if (a.init) win[k].load(init + (long long)(t + W - 1) * C);
+    for (int k = 0; k < W - 1; ++k) input(t0 - (W - 1) + k, before[k]);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+        next[i].zero();
+        if (t0 + i < t1) input(t0 + i, next[i]);
     }
-    Packed<float, VEC * W> wt;  // weight of channel j, tap k: element j W + k
+    Packed<float, VEC * W> weights;  // channel j, tap k at j W + k
     Packed<float, VEC> bias;
     if constexpr (VEC > 1) {
-        wt.load(a.weight + (long long)c * W);
+        weights.load(a.weight + (long long)c * W);
     } else {
 #pragma unroll
-        for (int k = 0; k < W; ++k) wt.w[k] = __float_as_uint(a.weight[(long long)c * W + k]);
+        for (int k = 0; k < W; ++k) weights.w[k] = __float_as_uint(a.weight[(long long)c * W + k]);
     }
     bias.zero();
     if (a.bias) bias.load(a.bias + c);
-    for (int t = t0; t < t1; t += kAhead) {
+    float2 wt[W][kPairs];
+#pragma unroll
+    for (int k = 0; k < W; ++k)
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j)
+            wt[k][j] = make_float2(weights.get(2 * j * W + k), VEC > 1 ? weights.get((2 * j + 1) * W + k) : 0.0f);
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) win[k][j] = before[k].pair(j);
+
+    const T* src = u + (long long)(t0 + kAhead) * a.u_row;
+    for (int left = t1 - t0; left > 0; left -= kAhead) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            win[W - 1 + i].zero();
-            if (t + i < t1) win[W - 1 + i].load(u + (long long)(t + i) * a.u_row);
-        }
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            if (t + i >= t1) break;
-            float v[VEC];
+            for (int j = 0; j < kPairs; ++j) win[W - 1][j] = next[i].pair(j);
+            if (kAhead + i < left) next[i].load(src);
+            src += a.u_row;
+            float v[2 * kPairs];
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                v[j] = bias.get(j);
+            for (int j = 0; j < kPairs; ++j) {
+                float2 s = bias.pair(j);
 #pragma unroll
-                for (int k = 0; k < W; ++k) v[j] = fmaf(wt.get(j * W + k), win[i + k].get(j), v[j]);
-                if (a.silu) v[j] = silu_f(v[j]);
+                for (int k = 0; k < W; ++k) s = fma2(wt[k][j], win[k][j], s);
+                if (a.silu) s = silu2(s);
+                v[2 * j] = s.x; v[2 * j + 1] = s.y;
+#pragma unroll
+                for (int k = 0; k < W - 1; ++k) win[k][j] = win[k + 1][j];
             }
             Packed<T, VEC> o;
             o.set(v);
-            o.store(out);
+            if (i < left) o.store(out);
             out += width;
-        }
-        // keep the last W - 1 inputs; after the last group, those of token t1 - 1
-        const int n = min(kAhead, t1 - t);
-#pragma unroll
-        for (int k = 0; k < W - 1; ++k) {
-            Packed<T, VEC> keep = win[k];
-#pragma unroll
-            for (int i = 1; i <= kAhead; ++i)
-                if (n == i) keep = win[k + i];
-            win[k] = keep;
         }
     }
     if (a.final_state && t1 == a.L) {
+        // read before the first is written: the single-token form shifts the state in place
         T* fs = static_cast<T*>(a.final_state) + (long long)b * (W - 1) * C + c;
+        if (a.L > 1) {
 #pragma unroll
-        for (int k = 0; k < W - 1; ++k) win[k].store(fs + (long long)k * C);
+            for (int k = 0; k < W - 1; ++k) input(a.L - (W - 1) + k, before[k]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < W - 2; ++k) before[k] = before[k + 1];
+            input(0, before[W - 2]);
+        }
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) before[k].store(fs + (long long)k * C);
     }
 }
 
-template <typename T, int VEC, int W>
+template <typename T, int VEC, int W, int kAhead>
 cudaError_t launch(const ConvArgs& a, const LaunchCtx& ctx)
 {
     const int cx = (a.C() / VEC + kThreads - 1) / kThreads;
-    // strips as long as leave about eight CTAs per SM, and 64 tokens at most
-    const long long want = (8ll * ctx.num_sms + (long long)cx * a.B - 1) / ((long long)cx * a.B);
-    int strip = (int)std::max(1ll, std::min<long long>(64, a.L / want));
+    // strips as long as leave about 32 CTAs per SM, and 32 tokens at most
+    const long long want = (32ll * ctx.num_sms + (long long)cx * a.B - 1) / ((long long)cx * a.B);
+    int strip = (int)std::max(1ll, std::min<long long>(32, a.L / want));
     strip = std::max(strip, (a.L + 65534) / 65535);  // the grid's y extent
     strip = (strip + kAhead - 1) / kAhead * kAhead;
     const int strips = (a.L + strip - 1) / strip;
-    const long long steps = (long long)a.H * std::min(strip, a.L);  // step sizes of a strip
-    const int dx = a.dt_raw ? (int)std::max(1ll, std::min(steps / (4 * kThreads), 8ll)) : 0;
-    conv_kernel<T, VEC, W><<<dim3(cx + dx, (unsigned)strips, a.B), kThreads, 0, ctx.stream>>>(a, strip, cx);
+    const int dx = a.dt_raw ? std::max(1, std::min(std::min(strip, a.L) / (kThreads / 32), 2)) : 0;
+    conv_kernel<T, VEC, W, kAhead><<<dim3(cx + dx, (unsigned)strips, a.B), kThreads, 0, ctx.stream>>>(a, strip, cx);
     return cudaGetLastError();
 }
 
-template <typename T, int VEC>
+template <typename T, int VEC, int kAhead>
 cudaError_t pick_width(const ConvArgs& a, const LaunchCtx& ctx)
 {
-    if (a.W == 2) return launch<T, VEC, 2>(a, ctx);
-    if (a.W == 3) return launch<T, VEC, 3>(a, ctx);
-    return launch<T, VEC, 4>(a, ctx);
+    if (a.W == 2) return launch<T, VEC, 2, kAhead>(a, ctx);
+    if (a.W == 3) return launch<T, VEC, 3, kAhead>(a, ctx);
+    return launch<T, VEC, 4, kAhead>(a, ctx);
+}
+
+// One token has nothing to load ahead (64 x 5376: 4.0 us against 4.9).
+template <typename T, int VEC>
+cudaError_t pick_ahead(const ConvArgs& a, const LaunchCtx& ctx)
+{
+    return a.L == 1 ? pick_width<T, VEC, 1>(a, ctx) : pick_width<T, VEC, 8>(a, ctx);
 }
 
 template <typename T>
 cudaError_t pick(const ConvArgs& a, const LaunchCtx& ctx)
 {
-    constexpr int V = 16 / (int)sizeof(T);
-    const bool vec = a.XC % V == 0 && a.GN % V == 0 && aligned_to(a.u, 16) && a.u_row % V == 0 &&
+    constexpr int V = 4;
+    const bool vec = a.XC % V == 0 && a.GN % V == 0 && aligned_to(a.u, V * sizeof(T)) && a.u_row % V == 0 &&
                      a.u_batch % V == 0;
-    return vec ? pick_width<T, V>(a, ctx) : pick_width<T, 1>(a, ctx);
+    return vec ? pick_ahead<T, V>(a, ctx) : pick_ahead<T, 1>(a, ctx);
 }
 
 }  // namespace
