@@ -203,9 +203,8 @@ ssd_status ssd_step(const void* x, const float* dt, const float* A, const void* 
  * follow the conventions at the top; strides count elements, and a strided
  * operand's last dimension is contiguous. Outputs must not overlap inputs or
  * each other except where an entry says so. Sums and statistics are fp32;
- * an output is rounded once, to nearest even. No entry here waits on the
- * device or needs a workspace but where it says so, so calls on different
- * streams may overlap freely.
+ * an output is rounded once, to nearest even. Calls on different streams may
+ * overlap freely, each with its own workspace where one is needed.
  */
 
 /*
@@ -247,13 +246,24 @@ ssd_status ssd_rms_norm(const void* x, const void* residual, const void* gate, i
  *   residual  [M, N]      `y_dtype` or NULL. May be y itself.
  *   y         [M, N]      `y_dtype`: SSD_F32 or SSD_BF16
  *   dtype     SSD_F32, SSD_BF16 or SSD_E4M3, of both operands
+ *   workspace  at least ssd_linear_workspace_size() bytes, which is 0 for bf16
+ *             and e4m3 operands with rows of 16-byte multiples from a 16-byte
+ *             base: those go to the tensor cores as they lie. Others are copied
+ *             there first when there are more than a few tokens (fp32 as three
+ *             bf16 parts, which keeps its 24 bits). It needs no clearing; calls
+ *             ordered on one stream may share it.
  *   Sizes: M, N >= 0 (0 is a no-op), K >= 1; M <= 2^30; N, K <= 2^20. x needs its
  *   element's alignment only; every other pointer is 16-byte aligned.
+ *   The result does not depend on the path beyond rounding: bf16 products are
+ *   exact in fp32 and added up there, where the tensor cores truncate; sums that
+ *   reach an fp32 output are joined, rounded, about every 512 products.
  */
+size_t ssd_linear_workspace_size(const void* x, int64_t x_stride, int M, int N, int K,
+                                 ssd_dtype dtype);
 ssd_status ssd_linear(const void* x, int64_t x_stride, const void* w, const float* x_scale,
                       const float* w_scale, const float* bias, const void* residual, void* y, int M,
                       int N, int K, ssd_activation act, ssd_dtype dtype, ssd_dtype y_dtype,
-                      ssd_stream_t stream);
+                      void* workspace, size_t workspace_bytes, ssd_stream_t stream);
 
 /*
  * ssd_conv — short causal convolution of every channel, and the cut of the
@@ -341,8 +351,9 @@ void ssd_set_forward_variant(int variant);
 
 /* Test hook: which kernel ssd_linear uses. 0 (the default) picks the fastest
  * for the sizes, 1 forces the SIMT kernel, 2 the tensor-core kernel for few
- * tokens, 3 the one for many (operands that TMA cannot address take the SIMT
- * kernel all the same). Other values restore 0. */
+ * tokens, 3 the one for many (the last two with the operands copied first where
+ * they have to be). Other values restore 0. ssd_linear_workspace_size() answers
+ * for the kernel set. */
 void ssd_set_linear_variant(int variant);
 
 #ifdef __cplusplus

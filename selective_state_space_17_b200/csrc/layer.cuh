@@ -63,8 +63,20 @@ struct LinearArgs {
     LinearType type;
     bool out_bf16;
 };
-cudaError_t linear(const LinearArgs& a, const LaunchCtx& ctx);       // the tensor cores where they can
-cudaError_t linear_simt(const LinearArgs& a, const LaunchCtx& ctx);  // any operands
+// Bytes of workspace linear() needs for these operands (0 for most).
+size_t linear_workspace_bytes(const LinearArgs& a);
+cudaError_t linear(const LinearArgs& a, void* workspace, const LaunchCtx& ctx);
+
+// Any operands; with only_if, only when that word is not zero (linear_simt.cu).
+cudaError_t linear_simt(const LinearArgs& a, const unsigned int* only_if, const LaunchCtx& ctx);
+// Few tokens, any operands.
+cudaError_t linear_rows(const LinearArgs& a, const LaunchCtx& ctx);
+// Rows of K elements copied to a pitch (elements) that TMA can address, zeros behind them.
+cudaError_t pack_rows(const void* src, long long stride, int rows, int K, LinearType type, void* dst, int pitch,
+                      const LaunchCtx& ctx);
+// Rows of K fp32 as three sections of bf16 each; *flag = 1 if a value does not split.
+cudaError_t split_rows(const float* src, long long stride, int rows, int K, void* dst, int section,
+                       unsigned int* flag, const LaunchCtx& ctx);
 void set_linear_variant(int variant);
 
 // Lets a kernel take up to `bytes` of dynamic shared memory on the current

@@ -96,6 +96,21 @@ ssd_status conv_call(const void* u, long long u_batch, long long u_row, const fl
     return launched(conv_forward(a, ctx));
 }
 
+// The checks of a product's sizes, and what decides its path.
+ssd_status linear_args(const void* x, int64_t x_stride, int M, int N, int K, ssd_dtype dtype, LinearArgs* a)
+{
+    if (M < 0 || N < 0 || K < 1) return SSD_ERR_INVALID_ARG;
+    if (dtype != SSD_E4M3 && !io_dtype(dtype)) return SSD_ERR_INVALID_ARG;
+    if (M > (1 << 30) || N > (1 << 20) || K > (1 << 20)) return SSD_ERR_UNSUPPORTED;
+    a->x = x;
+    a->x_stride = M > 1 ? x_stride : K;  // one row is as good as contiguous
+    a->M = M;
+    a->N = N;
+    a->K = K;
+    a->type = dtype == SSD_F32 ? LinearType::f32 : dtype == SSD_BF16 ? LinearType::bf16 : LinearType::e4m3;
+    return SSD_OK;
+}
+
 }  // namespace
 
 cudaError_t allow_smem(const void* kernel, int bytes)
@@ -154,40 +169,47 @@ ssd_status ssd_rms_norm(const void* x, const void* residual, const void* gate, i
     return launched(rms_norm(a, ctx));
 }
 
+size_t ssd_linear_workspace_size(const void* x, int64_t x_stride, int M, int N, int K, ssd_dtype dtype)
+{
+    LinearArgs a = {};
+    if (M < 1 || N < 1 || linear_args(x, x_stride, M, N, K, dtype, &a) != SSD_OK) return 0;
+    return linear_workspace_bytes(a);
+}
+
 ssd_status ssd_linear(const void* x, int64_t x_stride, const void* w, const float* x_scale,
                       const float* w_scale, const float* bias, const void* residual, void* y, int M,
                       int N, int K, ssd_activation act, ssd_dtype dtype, ssd_dtype y_dtype,
-                      ssd_stream_t stream)
+                      void* workspace, size_t workspace_bytes, ssd_stream_t stream)
 {
-    if (M < 0 || N < 0 || K < 1) return SSD_ERR_INVALID_ARG;
-    if (dtype != SSD_E4M3 && !io_dtype(dtype)) return SSD_ERR_INVALID_ARG;
+    LinearArgs a = {};
+    ssd_status st = linear_args(x, x_stride, M, N, K, dtype, &a);
+    if (st != SSD_OK) return st;
     if (!io_dtype(y_dtype)) return SSD_ERR_INVALID_ARG;
     if (act != SSD_ACT_NONE && act != SSD_ACT_SILU && act != SSD_ACT_GELU) return SSD_ERR_INVALID_ARG;
-    if (M > (1 << 30) || N > (1 << 20) || K > (1 << 20)) return SSD_ERR_UNSUPPORTED;
     if (M == 0 || N == 0) return SSD_OK;
     if (!x || !w || !y) return SSD_ERR_INVALID_ARG;
     if ((dtype == SSD_E4M3) != (x_scale != nullptr) || (dtype == SSD_E4M3) != (w_scale != nullptr))
         return SSD_ERR_INVALID_ARG;
     if (M > 1 && x_stride < K) return SSD_ERR_INVALID_ARG;
-    const void* ptrs[] = {w, x_scale, w_scale, bias, residual, y};
+    const void* ptrs[] = {w, x_scale, w_scale, bias, residual, y, workspace};
     for (const void* p : ptrs)
         if (!aligned_to(p, 16)) return SSD_ERR_MISALIGNED;
-    if (!aligned_to(x, dtype == SSD_E4M3 ? 1 : io_size(dtype))) return SSD_ERR_MISALIGNED;
     const size_t es = dtype == SSD_E4M3 ? 1 : io_size(dtype), ys = (size_t)M * N * io_size(y_dtype);
-    const Span out[] = {{y, ys}};
+    if (!aligned_to(x, es)) return SSD_ERR_MISALIGNED;
+    const size_t need = linear_workspace_bytes(a);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return SSD_ERR_WORKSPACE;
+    const Span out[] = {{y, ys}, {need ? workspace : nullptr, need}};
     const Span in[] = {{x, extent(M, x_stride, K, es)}, {w, (size_t)N * K * es}, {x_scale, (size_t)M * 4},
                        {w_scale, (size_t)N * 4}, {bias, (size_t)N * 4},
                        {residual == y ? nullptr : residual, ys}};
     if (any_overlap(out, in)) return SSD_ERR_INVALID_ARG;
     LaunchCtx ctx;
-    const ssd_status st = acquire_launch_ctx(reinterpret_cast<cudaStream_t>(stream), &ctx);
+    st = acquire_launch_ctx(reinterpret_cast<cudaStream_t>(stream), &ctx);
     if (st != SSD_OK) return st;
-    LinearArgs a;
-    a.x = x; a.x_stride = M > 1 ? x_stride : K; a.w = w; a.x_scale = x_scale; a.w_scale = w_scale; a.bias = bias;
-    a.residual = residual; a.y = y; a.M = M; a.N = N; a.K = K; a.act = act;
-    a.type = dtype == SSD_F32 ? LinearType::f32 : dtype == SSD_BF16 ? LinearType::bf16 : LinearType::e4m3;
+    a.w = w; a.x_scale = x_scale; a.w_scale = w_scale; a.bias = bias; a.residual = residual; a.y = y;
+    a.act = act;
     a.out_bf16 = y_dtype == SSD_BF16;
-    return launched(linear(a, ctx));
+    return launched(linear(a, workspace, ctx));
 }
 
 void ssd_set_linear_variant(int variant) { set_linear_variant(variant); }

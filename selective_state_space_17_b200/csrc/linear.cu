@@ -27,6 +27,27 @@ std::atomic<int> g_variant{0};  // test hook: 0 automatic, 1 SIMT, 2 few tokens,
 
 constexpr int kRowBytes = 128;  // bytes of an operand row in one stage
 
+// The K axis as the kernels walk it, in blocks of one stage: `sections` runs of
+// `per` blocks; section i reads x from column x_section(i) * cols on, w likewise.
+// One section for operands as they are; six for fp32 operands held as three bf16
+// sections each (see linear_split).
+struct Axis {
+    int per, sections, cols;
+    uint32_t x_sections, w_sections;  // two bits for each section
+    __host__ __device__ int blocks() const { return per * sections; }
+    __device__ __forceinline__ int x_col(int section) const { return (x_sections >> (2 * section) & 3) * cols; }
+    __device__ __forceinline__ int w_col(int section) const { return (w_sections >> (2 * section) & 3) * cols; }
+};
+
+// Operands that TMA can address: columns and pitch in elements.
+struct Operands {
+    const void* x;
+    const void* w;
+    long long x_cols, x_pitch, w_cols, w_pitch;
+    Axis axis;
+    const unsigned int* skip;  // with it, nothing is computed when the word is not zero
+};
+
 struct Epilogue {
     const float* x_scale;
     const float* w_scale;
@@ -59,10 +80,12 @@ struct Few {
 template <int BN, bool E4M3, typename O>
 __global__ void __launch_bounds__(128)
 linear_few_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
-                  const Epilogue e, int kblocks, int seg_blocks, uint32_t tmem_cols, unsigned int* status)
+                  const Epilogue e, const Axis axis, const unsigned int* skip, int seg_blocks, uint32_t tmem_cols,
+                  unsigned int* status)
 {
     using F = Few<BN>;
     constexpr int NS = F::kStages;
+    if (skip && *skip != 0) return;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(sm + F::kData);
@@ -74,8 +97,8 @@ linear_few_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
     const int splits = gridDim.x;
     const int rank = blockIdx.x;  // the cluster spans x: the rank within it
     const int n0 = blockIdx.y * 128, m0 = blockIdx.z * BN;
-    const int kb0 = (int)((long long)kblocks * rank / splits);
-    const int kb1 = (int)((long long)kblocks * (rank + 1) / splits);
+    const int kb0 = (int)((long long)axis.blocks() * rank / splits);
+    const int kb1 = (int)((long long)axis.blocks() * (rank + 1) / splits);
     const int count = kb1 - kb0;
 
     if (threadIdx.x == 0) {
@@ -100,16 +123,20 @@ linear_few_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
         if (elect_one_sync()) {
             prefetch_tensormap(&wmap);
             prefetch_tensormap(&xmap);
-            int issued = 0;
+            int issued = 0, section = kb0 / axis.per, block = kb0 - section * axis.per;
             for (; issued < count; ++issued) {
                 const int st = issued % NS;
                 if (issued >= NS) wait_or_abort(empty + st, ((issued / NS) - 1) & 1, abort_flag, status);
                 if (*abort_flag) break;
                 uint8_t* a = sm + st * F::kStageBytes;
-                const int k = (kb0 + issued) * (E4M3 ? kRowBytes : kRowBytes / 2);
+                const int k = block * (E4M3 ? kRowBytes : kRowBytes / 2);
                 mbar_arrive_expect_tx(full + st, F::kStageBytes);
-                tma_load_2d(a, &wmap, k, n0, full + st);
-                tma_load_2d(a + 128 * kRowBytes, &xmap, k, m0, full + st);
+                tma_load_2d(a, &wmap, axis.w_col(section) + k, n0, full + st);
+                tma_load_2d(a + 128 * kRowBytes, &xmap, axis.x_col(section) + k, m0, full + st);
+                if (++block == axis.per) {
+                    block = 0;
+                    ++section;
+                }
             }
             // loads in flight end before the CTA does (in abort mode the MMA warp
             // may not have waited for them)
@@ -226,12 +253,12 @@ linear_few_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
 }
 
 template <int BN, bool E4M3, typename O>
-cudaError_t launch_few(const LinearArgs& a, const Epilogue& e, int splits, const LaunchCtx& ctx)
+cudaError_t launch_few(const Operands& o, const Epilogue& e, int splits, const LaunchCtx& ctx)
 {
     using F = Few<BN>;
     const int es = E4M3 ? 1 : 2;
-    const int kblocks = (int)(((long long)a.K * es + kRowBytes - 1) / kRowBytes);
-    const int tn = (a.N + 127) / 128, tm = (a.M + BN - 1) / BN;
+    const int kblocks = o.axis.blocks();
+    const int tn = (e.N + 127) / 128, tm = (e.M + BN - 1) / BN;
     const int per = (kblocks + splits - 1) / splits;  // blocks of the longest part
     // about 512 bf16 products to a segment, as far as the accumulators go
     const int seg_blocks = std::max(8, (per + F::kMaxSegments - 1) / F::kMaxSegments);
@@ -239,8 +266,8 @@ cudaError_t launch_few(const LinearArgs& a, const Epilogue& e, int splits, const
     uint32_t cols = 32;
     while ((int)cols < segments * BN) cols *= 2;
     CUtensorMap wmap, xmap;
-    if (!make_map_rows(&wmap, a.w, E4M3, a.K, a.N, (uint64_t)a.K * es, 128) ||
-        !make_map_rows(&xmap, a.x, E4M3, a.K, a.M, (uint64_t)a.x_stride * es, BN))
+    if (!make_map_rows(&wmap, o.w, E4M3, o.w_cols, e.N, o.w_pitch * es, 128) ||
+        !make_map_rows(&xmap, o.x, E4M3, o.x_cols, e.M, o.x_pitch * es, BN))
         return cudaErrorInvalidValue;
     auto* kernel = linear_few_kernel<BN, E4M3, O>;
     cudaError_t err = allow_smem(reinterpret_cast<const void*>(kernel), F::kSmem);
@@ -256,23 +283,23 @@ cudaError_t launch_few(const LinearArgs& a, const Epilogue& e, int splits, const
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = splits > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, wmap, xmap, e, kblocks, seg_blocks, cols, ctx.status);
+    return cudaLaunchKernelEx(&cfg, kernel, wmap, xmap, e, o.axis, o.skip, seg_blocks, cols, ctx.status);
 }
 
 template <bool E4M3, typename O>
-cudaError_t few(const LinearArgs& a, const Epilogue& e, const LaunchCtx& ctx)
+cudaError_t few(const Operands& o, const Epilogue& e, const LaunchCtx& ctx)
 {
-    const int BN = a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 ? 64 : 128;
-    const int kblocks = (int)(((long long)a.K * (E4M3 ? 1 : 2) + kRowBytes - 1) / kRowBytes);
-    const long long tiles = (long long)((a.N + 127) / 128) * ((a.M + BN - 1) / BN);
+    const int BN = e.M <= 16 ? 16 : e.M <= 32 ? 32 : e.M <= 64 ? 64 : 128;
+    const int kblocks = o.axis.blocks();
+    const long long tiles = (long long)((e.N + 127) / 128) * ((e.M + BN - 1) / BN);
     // as many parts of K as two CTAs per SM hold at once, of two blocks at least
     int splits = (int)std::min<long long>(8, 2ll * ctx.num_sms / tiles);
     splits = std::max(1, std::min(splits, kblocks / 2));
     switch (BN) {
-    case 16: return launch_few<16, E4M3, O>(a, e, splits, ctx);
-    case 32: return launch_few<32, E4M3, O>(a, e, splits, ctx);
-    case 64: return launch_few<64, E4M3, O>(a, e, splits, ctx);
-    default: return launch_few<128, E4M3, O>(a, e, splits, ctx);
+    case 16: return launch_few<16, E4M3, O>(o, e, splits, ctx);
+    case 32: return launch_few<32, E4M3, O>(o, e, splits, ctx);
+    case 64: return launch_few<64, E4M3, O>(o, e, splits, ctx);
+    default: return launch_few<128, E4M3, O>(o, e, splits, ctx);
     }
 }
 
@@ -417,10 +444,11 @@ __device__ __forceinline__ void tile_at(const Tiles& t, long long i, int& im, in
 template <int BN, bool E4M3, typename O, bool SEG, bool WIDE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Many<BN, SEG>::kThreads, 1)
 linear_many_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
-                   const Epilogue e, const Tiles tiles, int kblocks, unsigned int* status)
+                   const Epilogue e, const Tiles tiles, const Axis axis, const unsigned int* skip, unsigned int* status)
 {
     using T = Many<BN, SEG>;
     constexpr int NS = T::kStages, NB = T::kBuffers;
+    if (skip && *skip != 0) return;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(sm + NS * T::kStageBytes);  // leader's: both CTAs' loads
@@ -433,6 +461,7 @@ linear_many_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int kblocks = axis.blocks();
     const int seg = SEG ? T::kSegBlocks : kblocks;  // K blocks of one accumulator
     const int segs = SEG ? (kblocks + seg - 1) / seg : 1;
 
@@ -465,17 +494,22 @@ linear_many_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                 int im, in;
                 tile_at(tiles, i, im, in);
                 const int m = im * 256 + (int)rank * 128, n = in * BN + (int)rank * T::kBRows;
+                int section = 0, block = 0;
                 for (int kb = 0; kb < kblocks; ++kb, ++it) {
                     const int st = (int)(it % NS);
                     if (it >= NS) wait_or_abort(empty + st, (uint32_t)((it / NS) - 1) & 1, abort_flag, status);
                     if (*abort_flag) break;
                     uint8_t* a = sm + st * T::kStageBytes;
-                    const int k = kb * (E4M3 ? kRowBytes : kRowBytes / 2);
+                    const int k = block * (E4M3 ? kRowBytes : kRowBytes / 2);
                     // the leader's barrier counts both CTAs' bytes
                     if (rank == 0) mbar_arrive_expect_tx(full + st, 2 * T::kStageBytes);
                     const uint32_t bar = map_rank(smem_addr(full + st), 0);
-                    tma_load_2d_pair(a, &xmap, k, m, bar);
-                    tma_load_2d_pair(a + 128 * kRowBytes, &wmap, k, n, bar);
+                    tma_load_2d_pair(a, &xmap, axis.x_col(section) + k, m, bar);
+                    tma_load_2d_pair(a + 128 * kRowBytes, &wmap, axis.w_col(section) + k, n, bar);
+                    if (++block == axis.per) {
+                        block = 0;
+                        ++section;
+                    }
                 }
             }
             // every stage loaded has been read by the MMAs: none is in flight when
@@ -591,60 +625,162 @@ linear_many_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
 }
 
 template <int BN, bool E4M3, typename O, bool SEG>
-cudaError_t launch_many(const LinearArgs& a, const Epilogue& e, const LaunchCtx& ctx)
+cudaError_t launch_many(const Operands& o, const Epilogue& e, const LaunchCtx& ctx)
 {
     using T = Many<BN, SEG>;
     const int es = E4M3 ? 1 : 2;
-    const int kblocks = (int)(((long long)a.K * es + kRowBytes - 1) / kRowBytes);
     Tiles t;
-    t.tm = (int)(((long long)a.M + 255) / 256);
-    t.tn = (a.N + BN - 1) / BN;
+    t.tm = (int)(((long long)e.M + 255) / 256);
+    t.tn = (e.N + BN - 1) / BN;
     t.group = 8;
     t.all = (long long)t.tm * t.tn;
     CUtensorMap wmap, xmap;
-    if (!make_map_rows(&wmap, a.w, E4M3, a.K, a.N, (uint64_t)a.K * es, T::kBRows) ||
-        !make_map_rows(&xmap, a.x, E4M3, a.K, a.M, (uint64_t)a.x_stride * es, 128))
+    if (!make_map_rows(&wmap, o.w, E4M3, o.w_cols, e.N, o.w_pitch * es, T::kBRows) ||
+        !make_map_rows(&xmap, o.x, E4M3, o.x_cols, e.M, o.x_pitch * es, 128))
         return cudaErrorInvalidValue;
-    const bool wide = (long long)a.N * sizeof(O) % 32 == 0 && aligned_to(a.y, 32) && aligned_to(a.residual, 32);
+    const bool wide = (long long)e.N * sizeof(O) % 32 == 0 && aligned_to(e.y, 32) && aligned_to(e.residual, 32);
     auto* kernel = wide ? linear_many_kernel<BN, E4M3, O, SEG, true> : linear_many_kernel<BN, E4M3, O, SEG, false>;
     cudaError_t err = allow_smem(reinterpret_cast<const void*>(kernel), T::kSmem);
     if (err != cudaSuccess) return err;
     const int pairs = (int)std::min<long long>(t.all, ctx.num_sms / 2);
-    kernel<<<2 * pairs, T::kThreads, T::kSmem, ctx.stream>>>(wmap, xmap, e, t, kblocks, ctx.status);
+    kernel<<<2 * pairs, T::kThreads, T::kSmem, ctx.stream>>>(wmap, xmap, e, t, o.axis, o.skip, ctx.status);
     return cudaGetLastError();
 }
 
 template <bool E4M3, typename O>
-cudaError_t many(const LinearArgs& a, const Epilogue& e, const LaunchCtx& ctx)
+cudaError_t many(const Operands& o, const Epilogue& e, const LaunchCtx& ctx)
 {
-    return launch_many<256, E4M3, O, sizeof(O) == 4 && !E4M3>(a, e, ctx);
+    return launch_many<256, E4M3, O, sizeof(O) == 4 && !E4M3>(o, e, ctx);
 }
 
 template <bool E4M3, typename O>
-cudaError_t run(const LinearArgs& a, const LaunchCtx& ctx)
+cudaError_t run(const Operands& o, const Epilogue& e, const LaunchCtx& ctx)
 {
-    const Epilogue e{a.x_scale, a.w_scale, a.bias, a.residual, a.y, a.M, a.N, a.act};
-    const bool use_many = g_variant ? g_variant == 3 : a.M >= 1024;
-    return use_many ? many<E4M3, O>(a, e, ctx) : few<E4M3, O>(a, e, ctx);
+    const bool use_many = g_variant ? g_variant == 3 : e.M >= 1024;
+    return use_many ? many<E4M3, O>(o, e, ctx) : few<E4M3, O>(o, e, ctx);
 }
 
+int element_bytes(const LinearArgs& a) { return a.type == LinearType::e4m3 ? 1 : a.type == LinearType::bf16 ? 2 : 4; }
+long long round_up(long long v, long long m) { return (v + m - 1) / m * m; }
+
 // TMA addresses rows of 16-byte multiples from 16-byte bases.
-bool tensor_core_rows(const LinearArgs& a)
+bool x_addressable(const LinearArgs& a)
 {
-    const int unit = a.type == LinearType::bf16 ? 8 : 16;
-    return a.type != LinearType::f32 && aligned_to(a.x, 16) && a.x_stride % unit == 0 && a.K % unit == 0;
+    return aligned_to(a.x, 16) && a.x_stride * element_bytes(a) % 16 == 0;
+}
+bool w_addressable(const LinearArgs& a) { return (long long)a.K * element_bytes(a) % 16 == 0; }
+
+// How a call's operands reach the kernels.
+enum class Path { direct, pack, split, rows, simt };
+
+// Operands that the tensor cores take as they lie go there. The others pay for
+// another copy of the weights, worth it from so many tokens on that the rows
+// kernel, which reads them as they are, is bound by its FMAs (ROWS_NOTE).
+Path path_of(const LinearArgs& a)
+{
+    if (g_variant == 1) return Path::simt;
+    if (a.type != LinearType::f32 && x_addressable(a) && w_addressable(a)) return Path::direct;
+    if (g_variant == 0 && a.M <= (a.type == LinearType::f32 ? 32 : 16)) return Path::rows;
+    return a.type == LinearType::f32 ? Path::split : Path::pack;
+}
+
+// Workspace: a flag (256 bytes), then x's copy, then w's.
+struct Copies {
+    long long x_pitch, w_pitch, cols;  // elements; cols: of one section
+    size_t x_at, w_at, bytes;
+};
+Copies copies_of(const LinearArgs& a, Path path)
+{
+    Copies c = {};
+    const int es = path == Path::split ? 2 : element_bytes(a), sections = path == Path::split ? 3 : 1;
+    c.cols = round_up(a.K, kRowBytes / es);
+    c.x_pitch = c.w_pitch = c.cols * sections;
+    c.x_at = 256;
+    const bool copy_x = path == Path::split || !x_addressable(a), copy_w = path == Path::split || !w_addressable(a);
+    c.w_at = c.x_at + (copy_x ? (size_t)round_up((long long)a.M * c.x_pitch * es, 256) : 0);
+    c.bytes = c.w_at + (copy_w ? (size_t)round_up((long long)a.N * c.w_pitch * es, 256) : 0);
+    return c;
+}
+
+template <bool E4M3>
+cudaError_t run_out(const Operands& o, const Epilogue& e, bool out_bf16, const LaunchCtx& ctx)
+{
+    return out_bf16 ? run<E4M3, __nv_bfloat16>(o, e, ctx) : run<E4M3, float>(o, e, ctx);
+}
+
+// fp32 operands on the bf16 tensor cores: x = x1 + x2 + x3 and w = w1 + w2 + w3
+// with 8 significant bits each, so
+//     x w = x1 w1 + (x1 w2 + x2 w1) + (x1 w3 + x2 w2 + x3 w1) + O(2^-24),
+// one product over six sections of K (and 6 of 1660 bf16 TFLOP/s against the
+// SIMT kernel's 37). Products of infinities do not split: when a value of the
+// operands does not fit bf16's range, the tensor-core kernel stands back and the
+// SIMT kernel computes the call.
+cudaError_t linear_split(const LinearArgs& a, const Epilogue& e, char* ws, const LaunchCtx& ctx)
+{
+    const Copies c = copies_of(a, Path::split);
+    unsigned int* flag = reinterpret_cast<unsigned int*>(ws);
+    cudaError_t err = cudaMemsetAsync(flag, 0, sizeof(*flag), ctx.stream);
+    if (err == cudaSuccess)
+        err = split_rows(static_cast<const float*>(a.x), a.x_stride, a.M, a.K, ws + c.x_at, (int)c.cols, flag, ctx);
+    if (err == cudaSuccess)
+        err = split_rows(static_cast<const float*>(a.w), a.K, a.N, a.K, ws + c.w_at, (int)c.cols, flag, ctx);
+    if (err != cudaSuccess) return err;
+    Operands o;
+    o.x = ws + c.x_at;
+    o.w = ws + c.w_at;
+    o.x_cols = o.x_pitch = o.w_cols = o.w_pitch = c.x_pitch;
+    // sections (x, w): (3, 1), (2, 2), (1, 3), (2, 1), (1, 2), (1, 1)
+    o.axis = {(int)(c.cols / (kRowBytes / 2)), 6, (int)c.cols,
+              2u | 1u << 2 | 0u << 4 | 1u << 6 | 0u << 8 | 0u << 10,
+              0u | 1u << 2 | 2u << 4 | 0u << 6 | 1u << 8 | 0u << 10};
+    o.skip = flag;
+    err = run_out<false>(o, e, a.out_bf16, ctx);
+    return err == cudaSuccess ? linear_simt(a, flag, ctx) : err;
 }
 
 }  // namespace
 
 void set_linear_variant(int variant) { g_variant = variant >= 0 && variant <= 3 ? variant : 0; }
 
-cudaError_t linear(const LinearArgs& a, const LaunchCtx& ctx)
+size_t linear_workspace_bytes(const LinearArgs& a)
 {
-    if (!tensor_core_rows(a) || g_variant == 1) return linear_simt(a, ctx);
-    if (a.type == LinearType::e4m3)
-        return a.out_bf16 ? run<true, __nv_bfloat16>(a, ctx) : run<true, float>(a, ctx);
-    return a.out_bf16 ? run<false, __nv_bfloat16>(a, ctx) : run<false, float>(a, ctx);
+    const Path path = path_of(a);
+    return path == Path::pack || path == Path::split ? copies_of(a, path).bytes : 0;
+}
+
+cudaError_t linear(const LinearArgs& a, void* workspace, const LaunchCtx& ctx)
+{
+    const Path path = path_of(a);
+    const Epilogue e{a.x_scale, a.w_scale, a.bias, a.residual, a.y, a.M, a.N, a.act};
+    char* ws = static_cast<char*>(workspace);
+    if (path == Path::simt) return linear_simt(a, nullptr, ctx);
+    if (path == Path::rows) return linear_rows(a, ctx);
+    if (path == Path::split) return linear_split(a, e, ws, ctx);
+    Operands o;
+    o.x = a.x;
+    o.w = a.w;
+    o.x_pitch = a.x_stride;
+    o.w_pitch = a.K;
+    o.x_cols = o.w_cols = a.K;
+    if (path == Path::pack) {
+        const Copies c = copies_of(a, path);
+        cudaError_t err = cudaSuccess;
+        if (!x_addressable(a)) {
+            o.x = ws + c.x_at;
+            o.x_pitch = c.x_pitch;
+            err = pack_rows(a.x, a.x_stride, a.M, a.K, a.type, ws + c.x_at, (int)c.x_pitch, ctx);
+        }
+        if (err == cudaSuccess && !w_addressable(a)) {
+            o.w = ws + c.w_at;
+            o.w_pitch = c.w_pitch;
+            err = pack_rows(a.w, a.K, a.N, a.K, a.type, ws + c.w_at, (int)c.w_pitch, ctx);
+        }
+        if (err != cudaSuccess) return err;
+    }
+    const int unit = kRowBytes / element_bytes(a);
+    o.axis = {(a.K + unit - 1) / unit, 1, 0, 0u, 0u};
+    o.skip = nullptr;
+    return a.type == LinearType::e4m3 ? run_out<true>(o, e, a.out_bf16, ctx) : run_out<false>(o, e, a.out_bf16, ctx);
 }
 
 }  // namespace ssd

@@ -23,8 +23,10 @@ ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2}
 _vp, _i, _i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
 lib.ssd_rms_norm.argtypes = [_vp] * 3 + [_i64] + [_vp] * 4 + [_i64, _i, _i, ctypes.c_float] + [_i] * 3 + [_vp]
 lib.ssd_rms_norm.restype = _i
-lib.ssd_linear.argtypes = [_vp, _i64] + [_vp] * 6 + [_i] * 6 + [_vp]
+lib.ssd_linear.argtypes = [_vp, _i64] + [_vp] * 6 + [_i] * 6 + [_vp, ctypes.c_size_t, _vp]
 lib.ssd_linear.restype = _i
+lib.ssd_linear_workspace_size.argtypes = [_vp, _i64] + [_i] * 4
+lib.ssd_linear_workspace_size.restype = ctypes.c_size_t
 lib.ssd_conv.argtypes = ([_vp, _i64, _i64, _vp, _vp, _vp, _i64, _i64] + [_vp] * 7 + [_i] * 9 + [_vp])
 lib.ssd_conv.restype = _i
 lib.ssd_conv_step.argtypes = [_vp, _i64, _vp, _vp, _vp, _i64] + [_vp] * 6 + [_i] * 8 + [_vp]
@@ -35,6 +37,7 @@ lib.ssd_set_linear_variant.restype = None
 
 _F32, _BF16, _E4M3 = torch.float32, torch.bfloat16, torch.float8_e4m3fn
 _IO = {_F32: SSD_F32, _BF16: SSD_BF16}
+_UNIT = {_BF16: 8, _E4M3: 16}  # elements of 16 bytes
 _OPERAND = {_F32: SSD_F32, _BF16: SSD_BF16, _E4M3: SSD_E4M3}
 
 
@@ -224,10 +227,20 @@ def linear(x, w, bias=None, activation: str = "none", residual=None, x_scale=Non
     M = 1
     for n in lead:
         M *= n
+    # operands that the tensor cores cannot take as they lie may need a copy; a
+    # workspace of this call alone lives as long as the stream needs it (also in
+    # a captured graph, whose memory pool keeps it)
+    pws, nbytes = None, 0
+    unit = _UNIT.get(dtype)
+    if unit is None or K % unit or x_stride % unit or px % 16:
+        nbytes = lib.ssd_linear_workspace_size(px, x_stride, M, N, K, code)
+        if nbytes:
+            workspace = x.new_empty((nbytes,), dtype=torch.uint8)
+            pws = workspace.data_ptr()
     rc = lib.ssd_linear(px, x_stride, pw, _arg(x_scale, "x_scale", _F32, dev, lead),
                         _arg(w_scale, "w_scale", _F32, dev, (N,)), _arg(bias, "bias", _F32, dev, (N,)),
                         _arg(residual, "residual", out_dtype, dev, shape), py, M, N, K, act, code,
-                        out_code, _raw_stream(dev))
+                        out_code, pws, nbytes, _raw_stream(dev))
     if rc:
         _check(rc, "ssd_linear")
     return y
@@ -338,6 +351,6 @@ def conv_step(u, weight, bias, state, H: int, P: int, G: int, N: int, dt=None, d
 
 
 def set_linear_variant(variant: int) -> None:
-    """Test hook: 0 automatic, 1 SIMT, 2 the tensor-core kernel for few tokens,
+    """Test hook (not for use beside other threads' calls): 0 automatic, 1 SIMT, 2 the tensor-core kernel for few tokens,
     3 the one for many (see include/ssd.h)."""
     lib.ssd_set_linear_variant(int(variant))

@@ -7,7 +7,7 @@ torch = pytest.importorskip("torch")
 
 F32, BF16, E4M3 = 0, 1, 2
 NONE, SILU, GELU = 0, 1, 2
-OK, INVALID, UNSUPPORTED, MISALIGNED = 0, 1, 2, 3
+OK, INVALID, UNSUPPORTED, MISALIGNED, WORKSPACE = 0, 1, 2, 3, 6
 
 
 @pytest.fixture(scope="module")
@@ -57,10 +57,11 @@ def test_norm_refusals(lib, kw, want):
 
 def linear(lib, **kw):
     a = dict(x=P(0), x_stride=32, w=P(1), xs=None, ws=None, bias=None, residual=None, y=P(2), M=4, N=48,
-             K=32, act=NONE, dtype=BF16, ydtype=BF16)
+             K=32, act=NONE, dtype=BF16, ydtype=BF16, ws_ptr=None, ws_bytes=0)
     a.update(kw)
     return lib.ssd_linear(a["x"], a["x_stride"], a["w"], a["xs"], a["ws"], a["bias"], a["residual"],
-                          a["y"], a["M"], a["N"], a["K"], a["act"], a["dtype"], a["ydtype"], None)
+                          a["y"], a["M"], a["N"], a["K"], a["act"], a["dtype"], a["ydtype"], a["ws_ptr"],
+                          a["ws_bytes"], None)
 
 
 @pytest.mark.parametrize("kw,want", [
@@ -72,11 +73,32 @@ def linear(lib, **kw):
     (dict(x_stride=31), INVALID), (dict(x=P(0) + 1), MISALIGNED), (dict(w=P(1) + 8), MISALIGNED),
     (dict(y=P(2) + 8), MISALIGNED), (dict(bias=P(3) + 4), MISALIGNED), (dict(residual=P(3) + 8), MISALIGNED),
     (dict(y=P(0)), INVALID), (dict(y=P(1) + 32), INVALID), (dict(residual=P(2) + 16), INVALID),
-    (dict(bias=P(2)), INVALID),
+    (dict(bias=P(2)), INVALID), (dict(ws_ptr=P(3) + 8), MISALIGNED),
+    # fp32 with more than a few tokens, and rows off 16 bytes, are copied first
+    (dict(M=64, dtype=F32, ydtype=F32), WORKSPACE), (dict(M=64, K=31, x_stride=32), WORKSPACE),
+    (dict(M=64, K=31, x_stride=31, ws_ptr=P(3), ws_bytes=1000), WORKSPACE),
+    (dict(M=64, dtype=F32, ydtype=F32, ws_ptr=P(2) + 256, ws_bytes=1 << 27), INVALID),  # over y
+    (dict(M=64, dtype=F32, ydtype=F32, ws_ptr=P(1), ws_bytes=1 << 27), INVALID),  # over w
     (dict(M=0, x=None, w=None, y=None), OK), (dict(N=0, x=None, w=None, y=None), OK),
 ])
 def test_linear_refusals(lib, kw, want):
     assert linear(lib, **kw) == want
+
+
+def test_linear_workspace_size(lib):
+    """256 bytes of flag, then copies of what TMA cannot address: rows of whole
+    128-byte blocks, three of them for an fp32 row."""
+    size = lib.ssd_linear_workspace_size
+    assert size(P(0), 2560, 64, 10576, 2560, BF16) == 0
+    assert size(P(0), 2576, 64, 48, 2560, E4M3) == 0
+    assert size(P(0), 2561, 8, 48, 2561, BF16) == 0  # few tokens: read as they lie
+    assert size(P(0), 2560, 8, 48, 2560, F32) == 0
+    row = 41 * 128  # 2561 bf16 elements are 5122 bytes
+    assert size(P(0), 2561, 64, 48, 2561, BF16) == 256 + (64 + 48) * row
+    assert size(P(0), 2561, 64, 48, 2560, BF16) == 256 + 64 * 40 * 128  # x's rows alone
+    assert size(P(0) + 2, 2560, 64, 48, 2560, BF16) == 256 + 64 * 40 * 128
+    assert size(P(0), 65, 64, 48, 65, F32) == 256 + (64 + 48) * 3 * 2 * 128
+    assert size(P(0), 64, 0, 48, 64, F32) == 0 and size(P(0), 64, 64, 48, 0, F32) == 0
 
 
 def conv(lib, **kw):

@@ -239,6 +239,69 @@ def test_linear_many_rows(ssd, M, N, K, dtype):
     check_linear(ssd, M, N, K, dtype, BF16, bias=True, act="silu", residual=True)
 
 
+@pytest.mark.parametrize("variant", [1, 2, 3])
+@pytest.mark.parametrize("dtype,out", [(F32, F32), (F32, BF16), (BF16, BF16), (BF16, F32), (E4M3, BF16), (E4M3, F32)])
+@pytest.mark.parametrize("M,N,K", [(1, 8, 16), (7, 100, 208), (130, 264, 1040), (300, 520, 77), (513, 1000, 640)])
+def test_linear_kernels(ssd, M, N, K, dtype, out, variant):
+    """Each kernel on the same products, whatever the automatic choice."""
+    ssd.layer.set_linear_variant(variant)
+    try:
+        check_linear(ssd, M, N, K, dtype, out, bias=True, act="gelu", residual=True)
+        check_linear(ssd, M, N, K, dtype, out, residual=True)
+    finally:
+        ssd.layer.set_linear_variant(0)
+
+
+@pytest.mark.parametrize("M", [3, 70, 1100])
+def test_linear_fp32_beyond_bf16(ssd, M):
+    """fp32 operands that three bf16 parts cannot hold: the products of
+    infinities, NaN and the largest values are those of fp32; and scales at the
+    ends of the range keep their 24 bits."""
+    g = gen(8)
+    x, w = randn(g, M, 96), randn(g, 72, 96)
+    w[5] = 0.5  # a row that one bf16 part holds: its other parts are zeros
+    bad = x.clone()
+    bad[0, 3], bad[1, 4], bad[2, 5] = float("inf"), float("nan"), 3.4e38
+    small = w * 2.0 ** -20
+    got = ssd.linear(bad, small)
+    want = bad.double() @ small.double().t()
+    size = bad.double().abs() @ small.double().abs().t()
+    check("y", got, want, torch.where(size.isfinite(), size * 220 * U, torch.zeros_like(size)))
+    again = ssd.linear(x, w)
+    check("y", again, x.double() @ w.double().t(), (x.double().abs() @ w.double().abs().t()) * 220 * U)
+    for sx, sw in ((2.0 ** 90, 2.0 ** -60), (2.0 ** -90, 2.0 ** 60)):
+        got = ssd.linear(x * sx, w * sw)
+        check("y", got, (x.double() * sx) @ (w.double() * sw).t(),
+              ((x.double() * sx).abs() @ (w.double() * sw).abs().t()) * 220 * U)
+
+
+def test_linear_fp32_captured_and_replayed(ssd):
+    """The copies of one graph's call are its own: two graphs replayed in turn,
+    and an eager call between, with a value that does not split in one of them."""
+    g = gen(9)
+    x, w = randn(g, 100, 130), randn(g, 90, 130)
+    graphs = []
+    ssd.linear(x, w)
+    for i in range(2):
+        graph = torch.cuda.CUDAGraph()
+        xi = x.clone()
+        with torch.cuda.graph(graph):
+            y = ssd.linear(xi, w)
+        graphs.append((graph, xi, y))
+    want = ssd.linear(x, w)
+    graphs[0][1][7, 7] = float("inf")
+    for _ in range(3):
+        for graph, _, _ in graphs:
+            graph.replay()
+        assert torch.equal(ssd.linear(x, w), want)
+        assert torch.equal(graphs[1][2], want)
+        y = graphs[0][2]
+        assert not y[7].isfinite().any()
+        rest = [m for m in range(100) if m != 7]
+        size = x.double().abs() @ w.double().abs().t()
+        check("y", y[rest], (x.double() @ w.double().t())[rest], (size * 300 * U)[rest])
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("offset,pitch", [(0, 320), (8, 328), (3, 301), (1, 298)])
 @pytest.mark.parametrize("M", [1, 40, 700])
