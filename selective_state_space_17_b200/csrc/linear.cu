@@ -14,6 +14,9 @@
 // the type, so the two types share all but the instruction.
 #include <algorithm>
 #include <atomic>
+#include <map>
+#include <mutex>
+#include <tuple>
 
 #include "layer.cuh"
 #include "sm100_mma.cuh"
@@ -66,6 +69,8 @@ struct Epilogue {
 // accumulator each: the tensor cores truncate each addition, a bias that grows
 // with the additions in a row (-4.7e-6 of the result after 5120 bf16 products,
 // -0.8e-6 after 1024), and the segments are joined with rounded additions.
+constexpr int kFewThreads = 256, kMostSplits = 8;
+
 template <int BN>
 struct Few {
     static constexpr int kStageBytes = 128 * kRowBytes + BN * kRowBytes;
@@ -78,7 +83,7 @@ struct Few {
 };
 
 template <int BN, bool E4M3, typename O>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(kFewThreads, 2)
 linear_few_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                   const Epilogue e, const Axis axis, const unsigned int* skip, int seg_blocks, uint32_t tmem_cols,
                   unsigned int* status)
@@ -169,11 +174,11 @@ linear_few_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
     // Every MMA has read its stages by now, so the stages' memory is free.
     float* red = reinterpret_cast<float*>(sm);
     const int segments = (count + seg_blocks - 1) / seg_blocks;
-    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+    // warps 0..3 and 4..7 take a lane quadrant each, every other 16 tokens
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const int tokens = min(BN, e.M - m0);
 #pragma unroll 1
-    for (int c = 0; c < BN; c += 16) {
-        if (c >= tokens) break;
+    for (int c = (warp >> 2) * 16; c < tokens; c += 32) {
         uint32_t v[16];
         tmem_ld16_sync(lanes + c, v);
         for (int s = 1; s < segments; ++s) {
@@ -183,70 +188,83 @@ linear_few_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
             for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(u[j]));
         }
 #pragma unroll
-        for (int j = 0; j < 16; ++j) red[(c + j) * 128 + warp * 32 + lane] = __uint_as_float(v[j]);
+        for (int j = 0; j < 16; ++j) red[(c + j) * 128 + (warp & 3) * 32 + lane] = __uint_as_float(v[j]);
     }
     tc_fence_before_sync();
+
+    // this thread's four channels of every token it joins: neighbours where rows
+    // of y and residual start on four elements, else a warp's width apart
+    const bool vec = (e.N & 3) == 0;
+    const int n = n0 + (vec ? lane * 4 : lane), step = vec ? 1 : 32;
+    float ws[4], bias[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int nj = min(n + j * step, e.N - 1);
+        ws[j] = E4M3 ? __ldg(e.w_scale + nj) : 1.0f;
+        bias[j] = e.bias ? __ldg(e.bias + nj) : 0.0f;
+    }
     if (splits > 1) cluster_sync();
     else __syncthreads();
     if (warp == 1) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, tmem_cols);
     }
-
     const uint32_t red_addr = smem_addr(red);
-    const bool vec = (e.N & 3) == 0;  // rows of y and residual then start on four elements
-    for (int t = rank + warp * splits; t < tokens; t += 4 * splits) {
+    const O* res = static_cast<const O*>(e.residual);
+#pragma unroll 1
+    for (int t = rank + warp * splits; t < tokens; t += (kFewThreads / 32) * splits) {
         const int m = m0 + t;
-        float v[4];
-        if (vec) {
-            const uint32_t at = red_addr + (uint32_t)(t * 128 + lane * 4) * 4;
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int r = 0; r < splits; ++r) {
-                const float4 p = ld_cluster_f4(splits > 1 ? map_rank(at, r) : at);
-                s.x += p.x; s.y += p.y; s.z += p.z; s.w += p.w;
-            }
-            v[0] = s.x; v[1] = s.y; v[2] = s.z; v[3] = s.w;
-        } else {
+        const long long row = (long long)m * e.N;
+        Packed<O, 4> r;
+        float rs[4];
+        if (res) {
+            if (vec && n < e.N) r.load(res + row + n);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const uint32_t at = red_addr + (uint32_t)(t * 128 + lane + 32 * j) * 4;
-                v[j] = 0.f;
-                for (int r = 0; r < splits; ++r) v[j] += ld_cluster_f1(splits > 1 ? map_rank(at, r) : at);
+                if (vec) rs[j] = r.get(j);
+                else if (n + j * step < e.N) rs[j] = static_cast<float>(res[row + n + j * step]);
             }
         }
-        const int n = n0 + (vec ? lane * 4 : lane), step = vec ? 1 : 32;
-        const float sx = E4M3 ? e.x_scale[m] : 1.0f;
-        const long long row = (long long)m * e.N;
-        const O* res = static_cast<const O*>(e.residual);
+        // every part is under way before the first is added
+        float4 p[kMostSplits];
+        const uint32_t at = red_addr + (uint32_t)(t * 128 + (vec ? lane * 4 : lane)) * 4;
+#pragma unroll
+        for (int k = 0; k < kMostSplits; ++k) {
+            if (k >= splits) break;
+            const uint32_t from = splits > 1 ? map_rank(at, k) : at;
+            if (vec) p[k] = ld_cluster_f4(from);
+            else p[k] = make_float4(ld_cluster_f1(from), ld_cluster_f1(from + 128), ld_cluster_f1(from + 256),
+                                    ld_cluster_f1(from + 384));
+        }
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < kMostSplits; ++k) {
+            if (k >= splits) break;
+            v[0] += p[k].x; v[1] += p[k].y; v[2] += p[k].z; v[3] += p[k].w;
+        }
+        const float sx = E4M3 ? __ldg(e.x_scale + m) : 1.0f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int nj = n + j * step;
-            if (nj >= e.N) continue;
-            if constexpr (E4M3) v[j] = v[j] * sx * __ldg(e.w_scale + nj);
-            if (e.bias) v[j] += __ldg(e.bias + nj);
-            v[j] = activate(v[j], e.act);
+            if constexpr (E4M3) v[j] = v[j] * sx * ws[j];
+            if (e.bias) v[j] += bias[j];
         }
-        O* y = static_cast<O*>(e.y) + row;
-        if (vec) {
-            if (n < e.N) {
-                if (res) {
-                    Packed<O, 4> p;
-                    p.load(res + row + n);
+        if (e.act != SSD_ACT_NONE) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) v[j] += p.get(j);
-                }
-                Packed<O, 4> p;
-                p.set(v);
-                p.store(y + n);
-            }
+            for (int j = 0; j < 4; ++j) v[j] = activate(v[j], e.act);
+        }
+        if (res) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] += rs[j];
+        }
+        O* y = static_cast<O*>(e.y) + row + n;
+        if (vec) {
+            Packed<O, 4> out;
+            out.set(v);
+            if (n < e.N) out.store(y);
         } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int nj = n + j * step;
-                if (nj >= e.N) continue;
-                if (res) v[j] += static_cast<float>(res[row + nj]);
-                io<O>::store(y + nj, v[j]);
-            }
+            for (int j = 0; j < 4; ++j)
+                if (n + j * step < e.N) io<O>::store(y + j * step, v[j]);
         }
     }
     if (splits > 1) cluster_sync();  // no CTA leaves while another reads its tile
@@ -274,7 +292,7 @@ cudaError_t launch_few(const Operands& o, const Epilogue& e, int splits, const L
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(splits, tn, tm);
-    cfg.blockDim = dim3(128);
+    cfg.blockDim = dim3(kFewThreads);
     cfg.dynamicSmemBytes = F::kSmem;
     cfg.stream = ctx.stream;
     cudaLaunchAttribute attr;
@@ -284,23 +302,6 @@ cudaError_t launch_few(const Operands& o, const Epilogue& e, int splits, const L
     cfg.attrs = &attr;
     cfg.numAttrs = splits > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, wmap, xmap, e, o.axis, o.skip, seg_blocks, cols, ctx.status);
-}
-
-template <bool E4M3, typename O>
-cudaError_t few(const Operands& o, const Epilogue& e, const LaunchCtx& ctx)
-{
-    const int BN = e.M <= 16 ? 16 : e.M <= 32 ? 32 : e.M <= 64 ? 64 : 128;
-    const int kblocks = o.axis.blocks();
-    const long long tiles = (long long)((e.N + 127) / 128) * ((e.M + BN - 1) / BN);
-    // as many parts of K as two CTAs per SM hold at once, of two blocks at least
-    int splits = (int)std::min<long long>(8, 2ll * ctx.num_sms / tiles);
-    splits = std::max(1, std::min(splits, kblocks / 2));
-    switch (BN) {
-    case 16: return launch_few<16, E4M3, O>(o, e, splits, ctx);
-    case 32: return launch_few<32, E4M3, O>(o, e, splits, ctx);
-    case 64: return launch_few<64, E4M3, O>(o, e, splits, ctx);
-    default: return launch_few<128, E4M3, O>(o, e, splits, ctx);
-    }
 }
 
 // ------------------------------------------------------------ many tokens
@@ -321,14 +322,19 @@ template <int BN, bool SEG>
 struct Many {
     static constexpr int kBRows = BN / 2;
     static constexpr int kStageBytes = (128 + kBRows) * kRowBytes;
-    static constexpr int kStages = (200 * 1024) / kStageBytes;
-    static constexpr int kSmem = 1024 + kStages * kStageBytes + 512;
+    static constexpr int kStages = (196 * 1024) / kStageBytes;
     static constexpr int kBuffers = 512 / BN;
     // warps of a lane quadrant share its columns: with SEG each holds its 64 in
     // registers, without it 128 in passing
     static constexpr int kParts = SEG ? BN / 64 : 2;
     static constexpr int kEpiWarps = 4 * kParts;
     static constexpr int kThreads = 128 + 32 * kEpiWarps;
+    // rows that do not start on 32 bytes leave through shared memory (see
+    // store_staged): 32 tokens x kTurn channels to a warp
+    static constexpr int kTurn = kEpiWarps > 8 ? 8 : 32;
+    static constexpr int kTurnBytes = 32 * (kTurn + 1) * 4 * kEpiWarps;
+    static constexpr int kSmem = 1024 + kStages * kStageBytes + kTurnBytes + 512;
+    static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
     static constexpr int kSegBlocks = 8;
 };
 
@@ -352,73 +358,109 @@ __device__ __forceinline__ void ldg4(const float* p, float* v)
     v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
 }
 
-// The epilogue of CH channels from n (a multiple of CH) of token m: the thread's
-// accumulator columns to y. WIDE: rows start on 32 bytes.
-template <int CH, bool E4M3, typename O, bool WIDE>
+// The epilogue of CH channels from n (a multiple of CH, all of them within the
+// row) of token m, rows that start on 32 bytes: the thread's accumulators to y.
+template <int CH, bool E4M3, typename O>
 __device__ __forceinline__ void store_row(const Epilogue& e, const void* residual, float* v, int m, int n, float sx)
 {
     const long long at = (long long)m * e.N + n;
     O* y = static_cast<O*>(e.y) + at;
     const O* res = static_cast<const O*>(residual);
-    if (WIDE && n + CH <= e.N) {
-        constexpr int kWords = CH * (int)sizeof(O) / 4;
-        uint32_t r[kWords];
-        if (res) {
+    constexpr int kWords = CH * (int)sizeof(O) / 4;
+    uint32_t r[kWords];
+    if (res) {
 #pragma unroll
-            for (int i = 0; i < kWords; i += 8) ld32(res + at + i * 4 / (int)sizeof(O), r + i);
+        for (int i = 0; i < kWords; i += 8) ld32(res + at + i * 4 / (int)sizeof(O), r + i);
+    }
+#pragma unroll
+    for (int c = 0; c < CH; c += 4) {
+        float b[4];
+        if constexpr (E4M3) {
+            ldg4(e.w_scale + n + c, b);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[c + j] = v[c + j] * sx * b[j];
         }
+        if (e.bias) {
+            ldg4(e.bias + n + c, b);
 #pragma unroll
-        for (int c = 0; c < CH; c += 4) {
-            float b[4];
-            if constexpr (E4M3) {
-                ldg4(e.w_scale + n + c, b);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[c + j] = v[c + j] * sx * b[j];
-            }
-            if (e.bias) {
-                ldg4(e.bias + n + c, b);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[c + j] += b[j];
-            }
+            for (int j = 0; j < 4; ++j) v[c + j] += b[j];
         }
-        if (e.act == SSD_ACT_SILU) {
+    }
+    if (e.act == SSD_ACT_SILU) {
 #pragma unroll
-            for (int j = 0; j < CH; ++j) v[j] = silu_f(v[j]);
-        } else if (e.act == SSD_ACT_GELU) {
-            // rolled for the sake of erfc's length; rotating the values by 8 keeps
-            // their indexes constants
+        for (int j = 0; j < CH; ++j) v[j] = silu_f(v[j]);
+    } else if (e.act == SSD_ACT_GELU) {
+        // rolled for the sake of erfc's length; rotating the values by 8 keeps
+        // their indexes constants
 #pragma unroll 1
-            for (int c = 0; c < CH; c += 8) {
+        for (int c = 0; c < CH; c += 8) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float t = gelu_f(v[j]);
+            for (int j = 0; j < 8; ++j) {
+                const float t = gelu_f(v[j]);
 #pragma unroll
-                    for (int i = j; i + 8 < CH; i += 8) v[i] = v[i + 8];
-                    v[CH - 8 + j] = t;
-                }
+                for (int i = j; i + 8 < CH; i += 8) v[i] = v[i + 8];
+                v[CH - 8 + j] = t;
             }
         }
-        Packed<O, CH> p;
-        if (res) {
-            Packed<O, CH> q;
+    }
+    Packed<O, CH> p;
+    if (res) {
+        Packed<O, CH> q;
 #pragma unroll
-            for (int i = 0; i < kWords; ++i) q.w[i] = r[i];
+        for (int i = 0; i < kWords; ++i) q.w[i] = r[i];
 #pragma unroll
-            for (int j = 0; j < CH; ++j) v[j] += q.get(j);
+        for (int j = 0; j < CH; ++j) v[j] += q.get(j);
+    }
+    p.set(v);
+#pragma unroll
+    for (int i = 0; i < kWords; i += 8) st32(y + i * 4 / (int)sizeof(O), p.w + i);
+}
+
+// The same for rows of any alignment, and for the last channels of a row: the
+// warp turns 32 tokens x CH channels round in shared memory (rows of CH + 1: no
+// bank conflicts), so that its lanes take neighbouring channels and every access
+// to y and residual is one run of a row. Called by the whole warp; m: the lane's
+// own token.
+template <int CH, bool E4M3, typename O>
+__device__ __forceinline__ void store_staged(const Epilogue& e, const void* residual, const float* v, float* turn, int m,
+                                             int n, float sx)
+{
+    const int lane = threadIdx.x & 31, m0 = m - lane;
+    constexpr int kRowsAtOnce = 32 / CH;  // of a row of CH channels
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < CH; ++j) turn[lane * (CH + 1) + j] = v[j];
+    __syncwarp();
+    const int c = lane % CH, nc = n + c;
+    const float ws = E4M3 ? __ldg(e.w_scale + min(nc, e.N - 1)) : 1.0f;
+    const float bias = e.bias ? __ldg(e.bias + min(nc, e.N - 1)) : 0.0f;
+    const O* res = static_cast<const O*>(residual);
+    constexpr int kBatch = 4;  // rows whose residuals are under way together
+#pragma unroll 1
+    for (int r0 = lane / CH; r0 < 32; r0 += kRowsAtOnce * kBatch) {
+        float rs[kBatch], f[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int r = r0 + i * kRowsAtOnce;
+            rs[i] = 0.0f;
+            if (res && m0 + r < e.M && nc < e.N) rs[i] = static_cast<float>(res[(long long)(m0 + r) * e.N + nc]);
         }
-        p.set(v);
 #pragma unroll
-        for (int i = 0; i < kWords; i += 8) st32(y + i * 4 / (int)sizeof(O), p.w + i);
-    } else {
+        for (int i = 0; i < kBatch; ++i) {
+            const int r = r0 + i * kRowsAtOnce;
+            f[i] = turn[r * (CH + 1) + c];
+            if constexpr (E4M3) f[i] = f[i] * __shfl_sync(0xffffffffu, sx, r) * ws;
+            if (e.bias) f[i] += bias;
+        }
+        if (e.act != SSD_ACT_NONE) {
 #pragma unroll
-        for (int j = 0; j < CH; ++j) {
-            if (n + j >= e.N) break;
-            float t = v[j];
-            if constexpr (E4M3) t = t * sx * __ldg(e.w_scale + n + j);
-            if (e.bias) t += __ldg(e.bias + n + j);
-            t = activate(t, e.act);
-            if (res) t += static_cast<float>(res[at + j]);
-            io<O>::store(y + j, t);
+            for (int i = 0; i < kBatch; ++i) f[i] = activate(f[i], e.act);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int r = r0 + i * kRowsAtOnce;
+            if (res) f[i] += rs[i];
+            if (m0 + r < e.M && nc < e.N) io<O>::store(static_cast<O*>(e.y) + (long long)(m0 + r) * e.N + nc, f[i]);
         }
     }
 }
@@ -451,7 +493,7 @@ linear_many_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     if (skip && *skip != 0) return;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(sm + NS * T::kStageBytes);  // leader's: both CTAs' loads
+    uint64_t* full = reinterpret_cast<uint64_t*>(sm + NS * T::kStageBytes + T::kTurnBytes);  // leader's: both CTAs' loads
     uint64_t* empty = full + NS;          // each CTA's
     uint64_t* acc_full = empty + NS;      // each CTA's
     uint64_t* acc_empty = acc_full + NB;  // leader's: both CTAs' epilogue warps
@@ -556,6 +598,7 @@ linear_many_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
         const int quad = warp & 3, part = (warp - 4) >> 2;
         constexpr int kCols = BN / T::kParts;
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + part * kCols;
+        float* turn = reinterpret_cast<float*>(sm + NS * T::kStageBytes) + (warp - 4) * 32 * (T::kTurn + 1);
         long long unit = 0;
         for (long long i = pair; i < tiles.all && !*abort_flag; i += pairs) {
             int im, in;
@@ -599,7 +642,12 @@ linear_many_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                         float f[32];
 #pragma unroll
                         for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
-                        if (m < e.M && !*abort_flag) store_row<32, E4M3, O, WIDE>(e, e.residual, f, m, n + c, sx);
+                        if (*abort_flag) continue;
+                        if (WIDE && n + c + 32 <= e.N) {
+                            if (m < e.M) store_row<32, E4M3, O>(e, e.residual, f, m, n + c, sx);
+                        } else if (n + c < e.N) {
+                            store_staged<32, E4M3, O>(e, e.residual, f, turn, m, n + c, sx);
+                        }
                     }
                 }
                 tc_fence_before_sync();
@@ -607,10 +655,17 @@ linear_many_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                 if (lane == 0) mbar_arrive_cluster(map_rank(smem_addr(acc_empty + buf), 0));
             }
             if constexpr (SEG) {
-                if (m < e.M && !*abort_flag) {
+                const void* residual = early ? nullptr : e.residual;
+                if (*abort_flag) continue;
+                if (WIDE && n + kCols <= e.N) {
+                    if (m < e.M) {
 #pragma unroll
-                    for (int c = 0; c < kCols; c += 8)
-                        store_row<8, E4M3, O, WIDE>(e, early ? nullptr : e.residual, sum + c, m, n + c, sx);
+                        for (int c = 0; c < kCols; c += 8) store_row<8, E4M3, O>(e, residual, sum + c, m, n + c, sx);
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < kCols; c += T::kTurn)
+                        if (n + c < e.N) store_staged<T::kTurn, E4M3, O>(e, residual, sum + c, turn, m, n + c, sx);
                 }
             }
         }
@@ -622,6 +677,13 @@ linear_many_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     cluster_sync();
     tc_fence_after_sync();
     if (warp == 2) tmem_dealloc_pair(tmem, 512);
+}
+
+// Whether rows of y and residual start on 32 bytes.
+template <typename O>
+bool wide_rows(const Epilogue& e)
+{
+    return (long long)e.N * sizeof(O) % 32 == 0 && aligned_to(e.y, 32) && aligned_to(e.residual, 32);
 }
 
 template <int BN, bool E4M3, typename O, bool SEG>
@@ -638,8 +700,7 @@ cudaError_t launch_many(const Operands& o, const Epilogue& e, const LaunchCtx& c
     if (!make_map_rows(&wmap, o.w, E4M3, o.w_cols, e.N, o.w_pitch * es, T::kBRows) ||
         !make_map_rows(&xmap, o.x, E4M3, o.x_cols, e.M, o.x_pitch * es, 128))
         return cudaErrorInvalidValue;
-    const bool wide = (long long)e.N * sizeof(O) % 32 == 0 && aligned_to(e.y, 32) && aligned_to(e.residual, 32);
-    auto* kernel = wide ? linear_many_kernel<BN, E4M3, O, SEG, true> : linear_many_kernel<BN, E4M3, O, SEG, false>;
+    auto* kernel = wide_rows<O>(e) ? linear_many_kernel<BN, E4M3, O, SEG, true> : linear_many_kernel<BN, E4M3, O, SEG, false>;
     cudaError_t err = allow_smem(reinterpret_cast<const void*>(kernel), T::kSmem);
     if (err != cudaSuccess) return err;
     const int pairs = (int)std::min<long long>(t.all, ctx.num_sms / 2);
@@ -647,17 +708,113 @@ cudaError_t launch_many(const Operands& o, const Epilogue& e, const LaunchCtx& c
     return cudaGetLastError();
 }
 
-template <bool E4M3, typename O>
-cudaError_t many(const Operands& o, const Epilogue& e, const LaunchCtx& ctx)
+// ------------------------------------------------------------------ choice
+
+// How many clusters of `splits` CTAs of the few-token kernel the device holds at
+// once (a GPC takes whole clusters only: 90, 44 and 30 of 3, 6 and 8 here); asks
+// the runtime once. Its answer counts one CTA per SM, of two.
+int active_clusters(const void* kernel, int smem, int splits, int num_sms)
 {
-    return launch_many<256, E4M3, O, sizeof(O) == 4 && !E4M3>(o, e, ctx);
+    static std::mutex mu;
+    static std::map<std::tuple<const void*, int, int>, int> known;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return num_sms;
+    std::lock_guard<std::mutex> lock(mu);
+    auto [at, fresh] = known.try_emplace({kernel, splits, dev}, 0);
+    if (!fresh) return at->second;
+    int n = 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(splits, 1024);
+    cfg.blockDim = dim3(kFewThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = splits;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (allow_smem(kernel, smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        n = std::max(1, num_sms / splits);
+    }
+    if (n * splits <= num_sms) n *= 2;
+    return at->second = n;
+}
+
+int tokens_per_tile(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
+
+// Estimated microseconds of a call, fitted to measurements of both kernels over
+// 1 to 2048 tokens and five weight shapes from 1024 x 2048 to 10576 x 2560, bf16
+// and e4m3 (off by a tenth on most, by a quarter at worst). A pair's tile takes
+// 0.31 us a block of K at 256 channels, where tensor cores and L2 balance, and
+// 0.215 at 128, where L2 bounds it; 2.5 and 1.5 us for its ends, and 4 more where
+// its rows leave through shared memory. The few-token
+// kernel takes a launch and the join (5.2 to 8 us with the tokens), and the
+// largest of its chain of stages (0.3 us a block), its traffic from L2 at 15
+// TB/s and the weights from HBM at 6 TB/s.
+float many_us(long long tm, int N, int BN, int kblocks, bool wide, int num_sms)
+{
+    const long long tiles = tm * ((N + BN - 1) / BN), pairs = num_sms / 2;
+    const float waves = (float)((tiles + pairs - 1) / pairs);
+    return 5.0f + waves * ((BN == 256 ? 0.31f * kblocks + 2.5f : 0.215f * kblocks + 1.5f) + (wide ? 0.0f : 4.0f));
+}
+float few_us(int BN, long long tiles, int N, int kblocks, int splits, int num_sms)
+{
+    const float waves = (float)((tiles * splits + 2ll * num_sms - 1) / (2ll * num_sms));
+    const float chain = waves * 0.3f * ((kblocks + splits - 1) / splits);
+    const float traffic = (float)tiles * kblocks * (128 + BN) * kRowBytes / 15e6f;
+    const float weights = (float)N * kblocks * kRowBytes / 6e6f;
+    return waves * (4.8f + 0.025f * BN) + std::max(chain, std::max(traffic, weights));
+}
+
+// The parts of K of a call of the few-token kernel: the fewest of the shortest
+// estimate among those whose clusters all run at once, two blocks to a part.
+template <int BN, bool E4M3, typename O>
+int few_splits(long long tiles, int N, int kblocks, int num_sms)
+{
+    const void* kernel = reinterpret_cast<const void*>(linear_few_kernel<BN, E4M3, O>);
+    int best = 1;
+    for (int s = 2; s <= std::min(kMostSplits, kblocks / 2); ++s) {
+        if (tiles * s > 2ll * num_sms || tiles > active_clusters(kernel, Few<BN>::kSmem, s, num_sms)) break;
+        if (few_us(BN, tiles, N, kblocks, s, num_sms) < few_us(BN, tiles, N, kblocks, best, num_sms)) best = s;
+    }
+    return best;
+}
+
+template <bool E4M3, typename O>
+int splits_for(int BN, long long tiles, int N, int kblocks, int num_sms)
+{
+    switch (BN) {
+    case 16: return few_splits<16, E4M3, O>(tiles, N, kblocks, num_sms);
+    case 32: return few_splits<32, E4M3, O>(tiles, N, kblocks, num_sms);
+    case 64: return few_splits<64, E4M3, O>(tiles, N, kblocks, num_sms);
+    default: return few_splits<128, E4M3, O>(tiles, N, kblocks, num_sms);
+    }
 }
 
 template <bool E4M3, typename O>
 cudaError_t run(const Operands& o, const Epilogue& e, const LaunchCtx& ctx)
 {
-    const bool use_many = g_variant ? g_variant == 3 : e.M >= 1024;
-    return use_many ? many<E4M3, O>(o, e, ctx) : few<E4M3, O>(o, e, ctx);
+    constexpr bool kSeg = sizeof(O) == 4 && !E4M3;
+    const int kblocks = o.axis.blocks(), BN = tokens_per_tile(e.M), sms = ctx.num_sms, variant = g_variant;
+    const long long tiles = (long long)((e.N + 127) / 128) * ((e.M + BN - 1) / BN), tm = ((long long)e.M + 255) / 256;
+    const bool wide = wide_rows<O>(e);
+    const float many256 = many_us(tm, e.N, 256, kblocks, wide, sms);
+    const float many128 = many_us(tm, e.N, 128, kblocks, wide, sms);
+    const bool fits = (e.M + BN - 1) / BN <= 65535;  // the grid's z extent
+    if (variant != 3 && fits) {
+        const int splits = splits_for<E4M3, O>(BN, tiles, e.N, kblocks, sms);
+        if (variant == 2 || few_us(BN, tiles, e.N, kblocks, splits, sms) <= std::min(many256, many128)) {
+            switch (BN) {
+            case 16: return launch_few<16, E4M3, O>(o, e, splits, ctx);
+            case 32: return launch_few<32, E4M3, O>(o, e, splits, ctx);
+            case 64: return launch_few<64, E4M3, O>(o, e, splits, ctx);
+            default: return launch_few<128, E4M3, O>(o, e, splits, ctx);
+            }
+        }
+    }
+    return many128 < many256 ? launch_many<128, E4M3, O, kSeg>(o, e, ctx) : launch_many<256, E4M3, O, kSeg>(o, e, ctx);
 }
 
 int element_bytes(const LinearArgs& a) { return a.type == LinearType::e4m3 ? 1 : a.type == LinearType::bf16 ? 2 : 4; }

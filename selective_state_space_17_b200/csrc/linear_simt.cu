@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) linear_rows_kernel(LinearArgs 
     const T* x = static_cast<const T*>(a.x);
     const T* w = static_cast<const T*>(a.w);
     float acc[MT][kCh] = {};
+#pragma unroll(MT > 4 ? 2 : 4)
     for (int k = (warp * 32 + lane) * VEC; k < a.K; k += 32 * kRowWarps * VEC) {
         float wv[kCh][VEC];
 #pragma unroll
@@ -161,49 +162,68 @@ template <typename T>
 cudaError_t launch_simt(const LinearArgs& a, const unsigned int* only_if, const LaunchCtx& ctx)
 {
     const long long tiles = (long long)((a.N + BN - 1) / BN) * ((a.M + BM - 1) / BM);
-    const unsigned grid = (unsigned)std::min<long long>(tiles, 4ll * ctx.num_sms);
+    const unsigned grid = (unsigned)std::min<long long>(tiles, 2ll * ctx.num_sms);
     if (a.out_bf16) linear_simt_kernel<T, __nv_bfloat16><<<grid, 256, 0, ctx.stream>>>(a, only_if);
     else linear_simt_kernel<T, float><<<grid, 256, 0, ctx.stream>>>(a, only_if);
     return cudaGetLastError();
 }
 
-// One warp to a row, its lanes along K.
+// A CTA to 1024 elements of a row, four to a thread, a CTA's width apart.
+constexpr int kPackThreads = 256, kPackEach = 4;
+
 template <typename T>
-__global__ void __launch_bounds__(256) pack_rows_kernel(const T* src, long long stride, int rows, int K, T* dst,
-                                                        int pitch)
+__global__ void __launch_bounds__(kPackThreads) pack_rows_kernel(const T* src, long long stride, int K, T* dst, int pitch)
 {
-    const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (row >= rows) return;
-    const T* s = src + row * stride;
-    T* d = dst + (long long)row * pitch;
-#pragma unroll 4
-    for (int k = lane; k < pitch; k += 32) d[k] = k < K ? s[k] : T(0);
+    const T* s = src + blockIdx.x * stride;
+    T* d = dst + (long long)blockIdx.x * pitch;
+    const int k0 = blockIdx.y * kPackThreads * kPackEach + threadIdx.x;
+    T v[kPackEach];
+#pragma unroll
+    for (int i = 0; i < kPackEach; ++i) {
+        const int k = k0 + i * kPackThreads;
+        v[i] = k < K ? s[k] : T(0);
+    }
+#pragma unroll
+    for (int i = 0; i < kPackEach; ++i) {
+        const int k = k0 + i * kPackThreads;
+        if (k < pitch) d[k] = v[i];
+    }
 }
 
 // fp32 as the sum of three bf16, 24 significant bits in all: each is what the
 // ones before it leave, rounded, and the differences are exact. What bf16 cannot
 // hold (infinities, NaN, values that round to infinity) sets the flag.
-__global__ void __launch_bounds__(256) split_rows_kernel(const float* src, long long stride, int rows, int K,
-                                                         __nv_bfloat16* dst, int section, unsigned int* flag)
+__global__ void __launch_bounds__(kPackThreads) split_rows_kernel(const float* src, long long stride, int K,
+                                                                  __nv_bfloat16* dst, int section, unsigned int* flag)
 {
-    const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (row >= rows) return;
-    const float* s = src + row * stride;
-    __nv_bfloat16* d = dst + (long long)row * 3 * section;
+    const float* s = src + blockIdx.x * stride;
+    __nv_bfloat16* d = dst + (long long)blockIdx.x * 3 * section;
+    const int k0 = blockIdx.y * kPackThreads * kPackEach + threadIdx.x;
+    float v[kPackEach];
     bool odd = false;
-#pragma unroll 4
-    for (int k = lane; k < section; k += 32) {
-        const float v = k < K ? s[k] : 0.0f;
-        odd |= !(fabsf(v) <= 3.38953139e38f);  // the largest bf16
-        const __nv_bfloat16 b1 = __float2bfloat16_rn(v);
-        const float r1 = v - __bfloat162float(b1);
+#pragma unroll
+    for (int i = 0; i < kPackEach; ++i) {
+        const int k = k0 + i * kPackThreads;
+        v[i] = k < K ? s[k] : 0.0f;
+        odd |= !(fabsf(v[i]) <= 3.38953139e38f);  // the largest bf16
+    }
+#pragma unroll
+    for (int i = 0; i < kPackEach; ++i) {
+        const int k = k0 + i * kPackThreads;
+        if (k >= section) break;
+        const __nv_bfloat16 b1 = __float2bfloat16_rn(v[i]);
+        const float r1 = v[i] - __bfloat162float(b1);
         const __nv_bfloat16 b2 = __float2bfloat16_rn(r1);
-        const __nv_bfloat16 b3 = __float2bfloat16_rn(r1 - __bfloat162float(b2));
         d[k] = b1;
         d[section + k] = b2;
-        d[2 * section + k] = b3;
+        d[2 * section + k] = __float2bfloat16_rn(r1 - __bfloat162float(b2));
     }
     if (odd) *flag = 1u;  // every writer writes the same
+}
+
+dim3 pack_grid(int rows, int pitch)
+{
+    return dim3(rows, (pitch + kPackThreads * kPackEach - 1) / (kPackThreads * kPackEach));
 }
 
 }  // namespace
@@ -231,12 +251,12 @@ cudaError_t linear_rows(const LinearArgs& a, const LaunchCtx& ctx)
 cudaError_t pack_rows(const void* src, long long stride, int rows, int K, LinearType type, void* dst, int pitch,
                       const LaunchCtx& ctx)
 {
-    const unsigned grid = (rows + 7) / 8;
+    const dim3 grid = pack_grid(rows, pitch);
     if (type == LinearType::bf16)
-        pack_rows_kernel<<<grid, 256, 0, ctx.stream>>>(static_cast<const uint16_t*>(src), stride, rows, K,
+        pack_rows_kernel<<<grid, kPackThreads, 0, ctx.stream>>>(static_cast<const uint16_t*>(src), stride, K,
                                                        static_cast<uint16_t*>(dst), pitch);
     else
-        pack_rows_kernel<<<grid, 256, 0, ctx.stream>>>(static_cast<const uint8_t*>(src), stride, rows, K,
+        pack_rows_kernel<<<grid, kPackThreads, 0, ctx.stream>>>(static_cast<const uint8_t*>(src), stride, K,
                                                        static_cast<uint8_t*>(dst), pitch);
     return cudaGetLastError();
 }
@@ -244,8 +264,8 @@ cudaError_t pack_rows(const void* src, long long stride, int rows, int K, Linear
 cudaError_t split_rows(const float* src, long long stride, int rows, int K, void* dst, int section,
                        unsigned int* flag, const LaunchCtx& ctx)
 {
-    split_rows_kernel<<<(rows + 7) / 8, 256, 0, ctx.stream>>>(src, stride, rows, K,
-                                                              static_cast<__nv_bfloat16*>(dst), section, flag);
+    split_rows_kernel<<<pack_grid(rows, section), kPackThreads, 0, ctx.stream>>>(
+        src, stride, K, static_cast<__nv_bfloat16*>(dst), section, flag);
     return cudaGetLastError();
 }
 
