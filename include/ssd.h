@@ -286,7 +286,7 @@ ssd_status ssd_linear(const void* x, int64_t x_stride, const void* w, const floa
  *             overlap initial_state.
  *   act       SSD_ACT_NONE or SSD_ACT_SILU
  *   Sizes: as ssd_forward for B, L, H, P, G, N (B*L == 0 is a no-op apart from
- *   final_state = initial_state or 0); B <= 65535; width in 2..4.
+ *   final_state = initial_state or 0); B <= 65535; L <= 2^30; width in 2..4.
  */
 ssd_status ssd_conv(const void* u, int64_t u_batch_stride, int64_t u_row_stride, const float* weight,
                     const float* bias, const void* dt_raw, int64_t dt_batch_stride,

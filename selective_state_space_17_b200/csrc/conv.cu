@@ -159,7 +159,7 @@ cudaError_t launch(const ConvArgs& a, const LaunchCtx& ctx)
     // strips as long as leave about 32 CTAs per SM, and 32 tokens at most
     const long long want = (32ll * ctx.num_sms + (long long)cx * a.B - 1) / ((long long)cx * a.B);
     int strip = (int)std::max(1ll, std::min<long long>(32, a.L / want));
-    strip = std::max(strip, (a.L + 65534) / 65535);  // the grid's y extent
+    strip = std::max(strip, a.L / 65535 + 1);  // the grid's y extent
     strip = (strip + kAhead - 1) / kAhead * kAhead;
     const int strips = (a.L + strip - 1) / strip;
     const int dx = a.dt_raw ? std::max(1, std::min(std::min(strip, a.L) / (kThreads / 32), 2)) : 0;

@@ -55,7 +55,7 @@ ssd_status conv_call(const void* u, long long u_batch, long long u_row, const fl
     if (st != SSD_OK) return st;
     if (width < 1 || u_batch < 0 || u_row < 0 || dt_batch < 0 || dt_row < 0) return SSD_ERR_INVALID_ARG;
     if (act != SSD_ACT_NONE && act != SSD_ACT_SILU) return SSD_ERR_INVALID_ARG;
-    if (width < 2 || width > 4 || B > 65535) return SSD_ERR_UNSUPPORTED;
+    if (width < 2 || width > 4 || B > 65535 || L > (1 << 30)) return SSD_ERR_UNSUPPORTED;
     const bool empty = (long long)B * L == 0;
     if (!empty && (!u || !weight || !x || !Bm || !Cm)) return SSD_ERR_INVALID_ARG;
     if (!empty && ((dt_raw != nullptr) != (dt != nullptr) || (dt_bias && !dt_raw))) return SSD_ERR_INVALID_ARG;

@@ -314,7 +314,7 @@ cudaError_t launch_few(const Operands& o, const Epilogue& e, int splits, const L
 // epilogue of one runs under the products of the next.
 //
 // SEG (fp32 outputs of bf16 operands): the epilogue warps hold the tile in registers and add up
-// accumulators of at most kSegBlocks K blocks with rounded additions, against
+// accumulators of at most kSegBlocks K blocks (768 products) with rounded additions, against
 // the bias of the tensor cores' truncated ones (see linear_few_kernel). A bf16
 // output's own rounding hides that bias, and products of e4m3 values, with eight
 // significant bits at most, lose next to nothing (measured 1e-8 at K = 5120).
@@ -335,7 +335,7 @@ struct Many {
     static constexpr int kTurnBytes = 32 * (kTurn + 1) * 4 * kEpiWarps;
     static constexpr int kSmem = 1024 + kStages * kStageBytes + kTurnBytes + 512;
     static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
-    static constexpr int kSegBlocks = 8;
+    static constexpr int kSegBlocks = 12;
 };
 
 // 32 bytes of one row (rows that allow it start on 32 bytes).

@@ -35,6 +35,7 @@ lib.ssd_conv_step.restype = _i
 lib.ssd_set_linear_variant.argtypes = [_i]
 lib.ssd_set_linear_variant.restype = None
 
+_Tensor = torch.Tensor
 _F32, _BF16, _E4M3 = torch.float32, torch.bfloat16, torch.float8_e4m3fn
 _IO = {_F32: SSD_F32, _BF16: SSD_BF16}
 _UNIT = {_BF16: 8, _E4M3: 16}  # elements of 16 bytes
@@ -53,10 +54,16 @@ def _arg(t, name, dtype, device, shape):
     goes to _need for its message."""
     if t is None:
         return None
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == device
             and t.shape == shape and t.is_contiguous()):
         _need(t, name, dtype, torch.device("cuda", device), shape)
     return t.data_ptr()
+
+
+def _sizes(where, *sizes):
+    """Refuses sizes that are no C int: ctypes would cut them to their low bits."""
+    if min(sizes) < 0 or max(sizes) > 0x7FFFFFFF:
+        raise ValueError(f"{where}: a size is out of range in {sizes}")
 
 
 def _io_code(t, name):
@@ -70,7 +77,7 @@ def _io_code(t, name):
 
 def _strided(t, name, dtype, device, shape):
     """The address of an operand that may be a view with a contiguous last dimension."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device and t.shape == shape):
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == device and t.shape == shape):
         _need(t.contiguous() if isinstance(t, torch.Tensor) else t, name, dtype, torch.device("cuda", device), shape)
     if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
@@ -135,6 +142,7 @@ def rms_norm(x, weight, residual=None, gate=None, eps: float = 1e-5, groups: int
         raise ValueError("x must have at least one dimension")
     D = shape[-1]
     rows = x.numel() // D if D else 0
+    _sizes("rms_norm", D, groups)
     px = _arg(x, "x", dtype, dev, shape)
     if weight is None:
         raise ValueError("weight is required")
@@ -227,6 +235,7 @@ def linear(x, w, bias=None, activation: str = "none", residual=None, x_scale=Non
     M = 1
     for n in lead:
         M *= n
+    _sizes("linear", M, N, K)
     # operands that the tensor cores cannot take as they lie may need a copy; a
     # workspace of this call alone lives as long as the stream needs it (also in
     # a captured graph, whose memory pool keeps it)
@@ -281,6 +290,7 @@ def conv(u, weight, bias, H: int, P: int, G: int, N: int, dt=None, dt_bias=None,
             return conv(u, weight, bias, H, P, G, N, dt, dt_bias, activation, initial_state,
                         final_state, return_final_state)
     dtype = u.dtype
+    _sizes("conv", H, P, G, N, *u.shape)
     C = H * P + 2 * G * N
     if u.dim() != 3 or u.shape[2] != C:
         raise ValueError(f"u must be [B, L, {C}], got shape {tuple(u.shape)}")
@@ -323,6 +333,7 @@ def conv_step(u, weight, bias, state, H: int, P: int, G: int, N: int, dt=None, d
         with _on(u, stream):
             return conv_step(u, weight, bias, state, H, P, G, N, dt, dt_bias, activation)
     dtype = u.dtype
+    _sizes("conv_step", H, P, G, N, *u.shape)
     C = H * P + 2 * G * N
     if u.dim() != 2 or u.shape[1] != C:
         raise ValueError(f"u must be [B, {C}], got shape {tuple(u.shape)}")

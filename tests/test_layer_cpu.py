@@ -114,7 +114,7 @@ def conv(lib, **kw):
 @pytest.mark.parametrize("kw,want", [
     (dict(H=3, G=2), INVALID), (dict(B=-1), INVALID), (dict(P=300), UNSUPPORTED), (dict(dtype=E4M3), INVALID),
     (dict(width=0), INVALID), (dict(width=1), UNSUPPORTED), (dict(width=5), UNSUPPORTED),
-    (dict(B=65536), UNSUPPORTED), (dict(act=GELU), INVALID), (dict(ur=-1), INVALID), (dict(ub=-1), INVALID),
+    (dict(B=65536), UNSUPPORTED), (dict(B=1, L=(1 << 30) + 1), UNSUPPORTED), (dict(act=GELU), INVALID), (dict(ur=-1), INVALID), (dict(ub=-1), INVALID),
     (dict(dr=-1), INVALID), (dict(db=-1), INVALID),
     *[(dict([(k, None)]), INVALID) for k in ("u", "weight", "x", "Bm", "Cm", "dt", "dt_raw")],
     *[(dict([(k, P(11) + 4)]), MISALIGNED)
@@ -160,6 +160,15 @@ def test_binding_rejects_host_tensors_and_bad_types():
         ssd.conv_step(torch.zeros(1, 160), torch.zeros(160, 4), None, torch.zeros(1, 3, 160), 2, 64, 1, 16)
     with pytest.raises(TypeError, match="torch.Tensor"):
         ssd.rms_norm([1.0], w)
+
+
+def test_binding_refuses_sizes_beyond_int():
+    """ctypes would cut them to 32 bits."""
+    from selective_state_space_17_b200.layer import _sizes
+    _sizes("x", 1, (1 << 31) - 1, 0)
+    for bad in (1 << 31, (1 << 32) + 5, -1):
+        with pytest.raises(ValueError, match="out of range"):
+            _sizes("x", 3, bad)
 
 
 def test_row_stride_of_views():
