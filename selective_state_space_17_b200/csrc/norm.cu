@@ -110,35 +110,32 @@ struct Factors {
     float first, second;
 };
 
-// Joins the lanes' (sum of squares, max |v w|) of a row: returns rho of this
-// thread's group, with Q8 over the row's scale s, which it stores. In one
-// factor, rho / s, but for rows so small that it overflows (a row of zeros).
-// red alternates between two buffers: a warp writes the next row's only after
+// The factors of a row of scale s: rho / s in one, but for rows so small that it
+// overflows (a row of zeros), where they are two.
+__device__ __forceinline__ Factors over_scale(float rho, float s)
+{
+    const float f = __fdividef(rho, s);
+    return isinf(f) ? Factors{rho, 1.0f / s} : Factors{f, 1.0f};
+}
+
+// Joins the lanes' (sum of squares, max |v w|) of a row and stores its scale with
+// Q8. red alternates between two buffers: a warp writes the next row's only after
 // this row's barrier, which follows every read of the one before.
+//
+// With one group, rho cancels in the 8-bit values: y / s = v w rho / (rho max |v w|
+// / 448) = v w (448 / max |v w|), two roundings, which leaves fewer values on the
+// wrong side of a border of e4m3 than rho and s would with theirs.
 template <bool Q8>
 __device__ __forceinline__ Factors join_row(float2 acc, const NormArgs& a, const Place& p, int wpg, float2* red,
-                                          long long row)
+                                            long long row)
 {
     acc = warp_sum_max<Q8>(acc);
-    float amax = 0.0f;  // max |y|
     const float inv_n = 1.0f / (float)p.Dg;
+    const bool writer = p.wr == 0 && p.lane == 0;
     if (p.wpr > 1) {
         if (p.lane == 0) red[p.warp] = acc;
         __syncthreads();
-        if (a.groups == 1) {
-            if (p.wpr <= 16) {
-                // both halves of the warp join the same sixteen
-                const int k = p.lane & 15;
-                const float2 e = k < p.wpr ? red[k] : both(0.0f);
-                acc.x = e.x;
-#pragma unroll
-                for (int o = 8; o; o >>= 1) acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o);
-                if constexpr (Q8) acc.y = warp_max(e.y);
-            } else {
-                acc = warp_sum_max<Q8>(p.lane < p.wpr ? red[p.lane] : both(0.0f));
-            }
-            if constexpr (Q8) amax = acc.y * rsqrtf(fmaf(acc.x, inv_n, a.eps));
-        } else {
+        if (a.groups > 1) {
             // lane g joins group g; its share of the maximum is rho_g max |v w|
             float2 t = both(0.0f);
             if (p.lane < a.groups) {
@@ -147,21 +144,34 @@ __device__ __forceinline__ Factors join_row(float2 acc, const NormArgs& a, const
                     t.x += e.x;
                     t.y = max_nan(t.y, e.y);
                 }
-                if constexpr (Q8) t.y *= rsqrtf(fmaf(t.x, inv_n, a.eps));
             }
-            acc.x = __shfl_sync(0xffffffffu, t.x, p.group);
-            if constexpr (Q8) amax = warp_max(t.y);
+            const float rho_lane = rsqrtf(fmaf(t.x, inv_n, a.eps));
+            const float rho = __shfl_sync(0xffffffffu, rho_lane, p.group);
+            if constexpr (!Q8) return {rho, 1.0f};
+            const float amax = warp_max(p.lane < a.groups ? t.y * rho_lane : 0.0f);
+            const float s = max_nan(amax / kE4m3Max, kScaleMin);
+            if (writer) a.scale[row] = s;
+            return over_scale(rho, s);
         }
-    } else if constexpr (Q8) {
-        amax = acc.y * rsqrtf(fmaf(acc.x, inv_n, a.eps));
+        if (p.wpr <= 16) {
+            // both halves of the warp join the same sixteen
+            const int k = p.lane & 15;
+            const float2 e = k < p.wpr ? red[k] : both(0.0f);
+            acc.x = e.x;
+#pragma unroll
+            for (int o = 8; o; o >>= 1) acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o);
+            if constexpr (Q8) acc.y = warp_max(e.y);
+        } else {
+            acc = warp_sum_max<Q8>(p.lane < p.wpr ? red[p.lane] : both(0.0f));
+        }
     }
     const float rho = rsqrtf(fmaf(acc.x, inv_n, a.eps));
     if constexpr (!Q8) return {rho, 1.0f};
-    const float s = max_nan(amax * (1.0f / kE4m3Max), kScaleMin);
-    if (p.wr == 0 && p.lane == 0) a.scale[row] = s;
-    const float f = __fdividef(rho, s);
-    if (isinf(f)) return {rho, 1.0f / s};
-    return {f, 1.0f};
+    const float amax = acc.y * rho;
+    if (writer) a.scale[row] = max_nan(amax / kE4m3Max, kScaleMin);
+    // the smallest scale, or NaN
+    if (!(amax >= kE4m3Max * kScaleMin)) return over_scale(rho, max_nan(amax / kE4m3Max, kScaleMin));
+    return {__fdividef(kE4m3Max, acc.y), 1.0f};
 }
 
 // v of one vector: x + r, x silu(z) or x.
