@@ -37,6 +37,8 @@ __device__ __forceinline__ float softplus_f(float v)
 template <typename T, int VEC, int W, int kAhead>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && VEC > 1 && kAhead > 1 ? 7 : 1) conv_kernel(ConvArgs a, int strip, int channel_ctas)
 {
+    wait_for_previous();
+    let_next_begin();
     const int b = blockIdx.z;
     const int t0 = blockIdx.y * strip, t1 = min(t0 + strip, a.L);
     if ((int)blockIdx.x >= channel_ctas) {
@@ -163,8 +165,8 @@ cudaError_t launch(const ConvArgs& a, const LaunchCtx& ctx)
     strip = (strip + kAhead - 1) / kAhead * kAhead;
     const int strips = (a.L + strip - 1) / strip;
     const int dx = a.dt_raw ? std::max(1, std::min(std::min(strip, a.L) / (kThreads / 32), 2)) : 0;
-    conv_kernel<T, VEC, W, kAhead><<<dim3(cx + dx, (unsigned)strips, a.B), kThreads, 0, ctx.stream>>>(a, strip, cx);
-    return cudaGetLastError();
+    return launch_overlapped(conv_kernel<T, VEC, W, kAhead>, dim3(cx + dx, strips, a.B), kThreads, 0, ctx.stream, 1, a,
+                             strip, cx);
 }
 
 template <typename T, int VEC, int kAhead>

@@ -85,6 +85,39 @@ cudaError_t allow_smem(const void* kernel, int bytes);
 
 inline bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
+// Programmatic dependent launch: a kernel launched by launch_overlapped may begin
+// while the one before it on the stream ends. Every thread waits here for that
+// one (all of it, and its writes) before it touches global memory.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// From here on the next kernel's CTAs may take the room this kernel leaves, once
+// every CTA of this kernel has come here. Called after what a CTA takes of its SM
+// for itself (tensor memory): the next kernel's CTAs hold theirs while they wait.
+__device__ __forceinline__ void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename T> struct same { using type = T; };  // its argument is not deduced
+template <typename T> using same_t = typename same<T>::type;
+
+template <typename... Args>
+cudaError_t launch_overlapped(void (*kernel)(Args...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                              int cluster, const same_t<Args>&... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = cluster;
+    attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+    cfg.attrs = attrs;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // v * sigmoid(v) = v / (1 + 2^(-v log2 e)). Where the power overflows, v < -88,
 // the reciprocal of inf is 0 and so is the result. The hardware's approximations
 // of 2^x and 1/x are off by at most 2 and 1 units of 2^-23, below every output's

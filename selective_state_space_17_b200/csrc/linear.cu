@@ -90,7 +90,10 @@ linear_few_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
 {
     using F = Few<BN>;
     constexpr int NS = F::kStages;
-    if (skip && *skip != 0) return;
+    if (skip) {
+        wait_for_previous();
+        if (*skip != 0) return;
+    }
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(sm + F::kData);
@@ -120,14 +123,18 @@ linear_few_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
         tmem_relinquish();
     }
     tc_fence_before_sync();
+    if (threadIdx.x == 32) {
+        prefetch_tensormap(&wmap);
+        prefetch_tensormap(&xmap);
+    }
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_ptr);
+    wait_for_previous();
+    let_next_begin();
 
     if (warp == 0) {
         if (elect_one_sync()) {
-            prefetch_tensormap(&wmap);
-            prefetch_tensormap(&xmap);
             int issued = 0, section = kb0 / axis.per, block = kb0 - section * axis.per;
             for (; issued < count; ++issued) {
                 const int st = issued % NS;
@@ -290,18 +297,8 @@ cudaError_t launch_few(const Operands& o, const Epilogue& e, int splits, const L
     auto* kernel = linear_few_kernel<BN, E4M3, O>;
     cudaError_t err = allow_smem(reinterpret_cast<const void*>(kernel), F::kSmem);
     if (err != cudaSuccess) return err;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(splits, tn, tm);
-    cfg.blockDim = dim3(kFewThreads);
-    cfg.dynamicSmemBytes = F::kSmem;
-    cfg.stream = ctx.stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = splits;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = splits > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, wmap, xmap, e, o.axis, o.skip, seg_blocks, cols, ctx.status);
+    return launch_overlapped(kernel, dim3(splits, tn, tm), kFewThreads, F::kSmem, ctx.stream, splits, wmap, xmap, e, o.axis,
+                             o.skip, seg_blocks, cols, ctx.status);
 }
 
 // ------------------------------------------------------------ many tokens
@@ -490,7 +487,10 @@ linear_many_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
 {
     using T = Many<BN, SEG>;
     constexpr int NS = T::kStages, NB = T::kBuffers;
-    if (skip && *skip != 0) return;
+    if (skip) {
+        wait_for_previous();
+        if (*skip != 0) return;
+    }
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(sm + NS * T::kStageBytes + T::kTurnBytes);  // leader's: both CTAs' loads
@@ -523,14 +523,18 @@ linear_many_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     if (warp == 2) tmem_alloc_pair(tmem_ptr, 512);
     tc_fence_before_sync();
     __syncthreads();
+    if (threadIdx.x == 32) {
+        prefetch_tensormap(&wmap);
+        prefetch_tensormap(&xmap);
+    }
     cluster_sync();  // barriers of both CTAs are set up
     tc_fence_after_sync();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_ptr);
+    wait_for_previous();
+    let_next_begin();
 
     if (warp == 0) {
         if (elect_one_sync()) {
-            prefetch_tensormap(&wmap);
-            prefetch_tensormap(&xmap);
             long long it = 0;
             for (long long i = pair; i < tiles.all && !*abort_flag; i += pairs) {
                 int im, in;
@@ -704,8 +708,9 @@ cudaError_t launch_many(const Operands& o, const Epilogue& e, const LaunchCtx& c
     cudaError_t err = allow_smem(reinterpret_cast<const void*>(kernel), T::kSmem);
     if (err != cudaSuccess) return err;
     const int pairs = (int)std::min<long long>(t.all, ctx.num_sms / 2);
-    kernel<<<2 * pairs, T::kThreads, T::kSmem, ctx.stream>>>(wmap, xmap, e, t, o.axis, o.skip, ctx.status);
-    return cudaGetLastError();
+    // the kernel's own attribute makes the pairs clusters of two
+    return launch_overlapped(kernel, 2 * pairs, T::kThreads, T::kSmem, ctx.stream, 1, wmap, xmap, e, t, o.axis, o.skip,
+                             ctx.status);
 }
 
 // ------------------------------------------------------------------ choice

@@ -246,6 +246,8 @@ __global__ void __launch_bounds__(VPT * VEC > 8 ? 512 : 1024, shared_weights(MOD
     constexpr bool kShared = shared_weights(MODE, VPT * VEC);
     constexpr int kPairs = (VEC + 1) / 2;
     Packed<float, VEC> w[VPT];
+    wait_for_previous();
+    let_next_begin();
     long long row = p.row0();
     if (row >= a.rows) return;
     auto load = [&](long long r) {
@@ -331,6 +333,8 @@ __global__ void __launch_bounds__(1024) rms_norm_wide_kernel(NormArgs a, int wpg
     constexpr int kPairs = (VEC + 1) / 2;
     const Place p(a, wpg, VEC);
     int buf = 0;
+    wait_for_previous();
+    let_next_begin();
     for (long long row = p.row0(); row < a.rows; row += p.row_step(), buf ^= 1) {
         const long long base = row * a.D + p.gbase, zbase = row * a.gate_stride + p.gbase;
         Operands<T, R, MODE, VEC> in;
@@ -378,9 +382,10 @@ cudaError_t launch(const NormArgs& a, const LaunchCtx& ctx)
     const long long cap = (long long)ctx.num_sms * std::max(1, 1024 / threads);
     const unsigned grid = (unsigned)std::min(ctas, cap);
     const size_t smem = shared_weights(MODE, VPT * VEC) ? sizeof(float) * VPT * VEC * threads : 0;
-    if constexpr (VPT > 0) rms_norm_kernel<T, R, MODE, Q8, VEC, VPT><<<grid, threads, smem, ctx.stream>>>(a, wpg);
-    else rms_norm_wide_kernel<T, R, MODE, Q8, VEC><<<grid, threads, 0, ctx.stream>>>(a, wpg);
-    return cudaGetLastError();
+    if constexpr (VPT > 0)
+        return launch_overlapped(rms_norm_kernel<T, R, MODE, Q8, VEC, VPT>, grid, threads, smem, ctx.stream, 1, a, wpg);
+    else
+        return launch_overlapped(rms_norm_wide_kernel<T, R, MODE, Q8, VEC>, grid, threads, 0, ctx.stream, 1, a, wpg);
 }
 
 // The widest access that every row allows (16 bytes of the I/O dtype), and the
