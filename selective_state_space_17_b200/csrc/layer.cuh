@@ -5,6 +5,8 @@
 
 #include <cuda_fp8.h>
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace ssd {
@@ -80,8 +82,16 @@ cudaError_t split_rows(const float* src, long long stride, int rows, int K, void
 void set_linear_variant(int variant);
 
 // Lets a kernel take up to `bytes` of dynamic shared memory on the current
-// device; asks the runtime once per kernel, device and size (layer_api.cu).
-cudaError_t allow_smem(const void* kernel, int bytes);
+// device; `done`, one per kernel and size, holds the devices asked already.
+inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (done.load(std::memory_order_relaxed) >> (dev & 63) & 1)) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
+    return e;
+}
 
 inline bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 

@@ -2,10 +2,6 @@
 // checks and dispatch. Declarations and contracts are in include/ssd.h.
 #include <math.h>
 
-#include <mutex>
-#include <set>
-#include <tuple>
-
 #include "layer.cuh"
 
 namespace ssd {
@@ -112,21 +108,6 @@ ssd_status linear_args(const void* x, int64_t x_stride, int M, int N, int K, ssd
 }
 
 }  // namespace
-
-cudaError_t allow_smem(const void* kernel, int bytes)
-{
-    static std::mutex mu;
-    static std::set<std::tuple<const void*, int, int>> done;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    std::lock_guard<std::mutex> lock(mu);
-    const auto key = std::make_tuple(kernel, dev, bytes);
-    if (done.count(key)) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) done.insert(key);
-    return e;
-}
 
 }  // namespace ssd
 

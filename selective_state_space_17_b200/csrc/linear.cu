@@ -14,9 +14,6 @@
 // the type, so the two types share all but the instruction.
 #include <algorithm>
 #include <atomic>
-#include <map>
-#include <mutex>
-#include <tuple>
 
 #include "layer.cuh"
 #include "sm100_mma.cuh"
@@ -71,24 +68,27 @@ struct Epilogue {
 // -0.8e-6 after 1024), and the segments are joined with rounded additions.
 constexpr int kFewThreads = 256, kMostSplits = 8;
 
-template <int BN>
+// DEEP: one CTA per SM with all of its shared memory, for calls of no more CTAs
+// than SMs, whose stages in flight then are what hides the latency of a load
+// (1003 x 1777 x 1000, 112 CTAs of 16 blocks: DEEP_NOTE).
+template <int BN, bool DEEP>
 struct Few {
     static constexpr int kStageBytes = 128 * kRowBytes + BN * kRowBytes;
     // two CTAs per SM, whose loads in flight together cover HBM's latency
-    static constexpr int kStages = std::min(6, (110 * 1024) / kStageBytes);
+    static constexpr int kStages = DEEP ? (200 * 1024) / kStageBytes : std::min(6, (110 * 1024) / kStageBytes);
     static constexpr int kRedBytes = BN * 128 * 4;
     static constexpr int kData = std::max(kStages * kStageBytes, kRedBytes);
     static constexpr int kSmem = 1024 + kData + 256;
     static constexpr int kMaxSegments = BN >= 128 ? 2 : 4;
 };
 
-template <int BN, bool E4M3, typename O>
+template <int BN, bool E4M3, typename O, bool DEEP>
 __global__ void __launch_bounds__(kFewThreads, 2)
 linear_few_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                   const Epilogue e, const Axis axis, const unsigned int* skip, int seg_blocks, uint32_t tmem_cols,
                   unsigned int* status)
 {
-    using F = Few<BN>;
+    using F = Few<BN, DEEP>;
     constexpr int NS = F::kStages;
     if (skip) {
         wait_for_previous();
@@ -277,10 +277,10 @@ linear_few_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
     if (splits > 1) cluster_sync();  // no CTA leaves while another reads its tile
 }
 
-template <int BN, bool E4M3, typename O>
-cudaError_t launch_few(const Operands& o, const Epilogue& e, int splits, const LaunchCtx& ctx)
+template <int BN, bool E4M3, typename O, bool DEEP>
+cudaError_t launch_few_as(const Operands& o, const Epilogue& e, int splits, const LaunchCtx& ctx)
 {
-    using F = Few<BN>;
+    using F = Few<BN, DEEP>;
     const int es = E4M3 ? 1 : 2;
     const int kblocks = o.axis.blocks();
     const int tn = (e.N + 127) / 128, tm = (e.M + BN - 1) / BN;
@@ -294,8 +294,9 @@ cudaError_t launch_few(const Operands& o, const Epilogue& e, int splits, const L
     if (!make_map_rows(&wmap, o.w, E4M3, o.w_cols, e.N, o.w_pitch * es, 128) ||
         !make_map_rows(&xmap, o.x, E4M3, o.x_cols, e.M, o.x_pitch * es, BN))
         return cudaErrorInvalidValue;
-    auto* kernel = linear_few_kernel<BN, E4M3, O>;
-    cudaError_t err = allow_smem(reinterpret_cast<const void*>(kernel), F::kSmem);
+    auto* kernel = linear_few_kernel<BN, E4M3, O, DEEP>;
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t err = allow_smem(reinterpret_cast<const void*>(kernel), F::kSmem, allowed);
     if (err != cudaSuccess) return err;
     return launch_overlapped(kernel, dim3(splits, tn, tm), kFewThreads, F::kSmem, ctx.stream, splits, wmap, xmap, e, o.axis,
                              o.skip, seg_blocks, cols, ctx.status);
@@ -431,34 +432,38 @@ __device__ __forceinline__ void store_staged(const Epilogue& e, const void* resi
     const int c = lane % CH, nc = n + c;
     const float ws = E4M3 ? __ldg(e.w_scale + min(nc, e.N - 1)) : 1.0f;
     const float bias = e.bias ? __ldg(e.bias + min(nc, e.N - 1)) : 0.0f;
-    const O* res = static_cast<const O*>(residual);
-    constexpr int kBatch = 4;  // rows whose residuals are under way together
+    constexpr int kBatch = 8 < CH ? 8 : CH;  // rows under way together
+    const int first = lane / CH;
+    const int rows = nc < e.N ? min(32, e.M - m0) : 0;  // those of this lane's channel
+    const long long at = (long long)(m0 + first) * e.N + nc, step = (long long)kRowsAtOnce * e.N;
+    const O* res = residual ? static_cast<const O*>(residual) + at : nullptr;
+    O* y = static_cast<O*>(e.y) + at;
 #pragma unroll 1
-    for (int r0 = lane / CH; r0 < 32; r0 += kRowsAtOnce * kBatch) {
+    for (int r0 = first; r0 < 32; r0 += kRowsAtOnce * kBatch) {
         float rs[kBatch], f[kBatch];
+        if (res) {
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int r = r0 + i * kRowsAtOnce;
-            rs[i] = 0.0f;
-            if (res && m0 + r < e.M && nc < e.N) rs[i] = static_cast<float>(res[(long long)(m0 + r) * e.N + nc]);
+            for (int i = 0; i < kBatch; ++i, res += step)
+                rs[i] = r0 + i * kRowsAtOnce < rows ? static_cast<float>(*res) : 0.0f;
         }
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             const int r = r0 + i * kRowsAtOnce;
             f[i] = turn[r * (CH + 1) + c];
             if constexpr (E4M3) f[i] = f[i] * __shfl_sync(0xffffffffu, sx, r) * ws;
-            if (e.bias) f[i] += bias;
+            f[i] += bias;
         }
         if (e.act != SSD_ACT_NONE) {
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) f[i] = activate(f[i], e.act);
         }
+        if (res) {
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int r = r0 + i * kRowsAtOnce;
-            if (res) f[i] += rs[i];
-            if (m0 + r < e.M && nc < e.N) io<O>::store(static_cast<O*>(e.y) + (long long)(m0 + r) * e.N + nc, f[i]);
+            for (int i = 0; i < kBatch; ++i) f[i] += rs[i];
         }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i, y += step)
+            if (r0 + i * kRowsAtOnce < rows) io<O>::store(y, f[i]);
     }
 }
 
@@ -704,8 +709,12 @@ cudaError_t launch_many(const Operands& o, const Epilogue& e, const LaunchCtx& c
     if (!make_map_rows(&wmap, o.w, E4M3, o.w_cols, e.N, o.w_pitch * es, T::kBRows) ||
         !make_map_rows(&xmap, o.x, E4M3, o.x_cols, e.M, o.x_pitch * es, 128))
         return cudaErrorInvalidValue;
-    auto* kernel = wide_rows<O>(e) ? linear_many_kernel<BN, E4M3, O, SEG, true> : linear_many_kernel<BN, E4M3, O, SEG, false>;
-    cudaError_t err = allow_smem(reinterpret_cast<const void*>(kernel), T::kSmem);
+    auto* kernel = linear_many_kernel<BN, E4M3, O, SEG, true>;
+    if constexpr (!(SEG && BN == 256)) {
+        if (!wide_rows<O>(e)) kernel = linear_many_kernel<BN, E4M3, O, SEG, false>;
+    }
+    static std::atomic<uint64_t> allowed[2];
+    cudaError_t err = allow_smem(reinterpret_cast<const void*>(kernel), T::kSmem, allowed[wide_rows<O>(e)]);
     if (err != cudaSuccess) return err;
     const int pairs = (int)std::min<long long>(t.all, ctx.num_sms / 2);
     // the kernel's own attribute makes the pairs clusters of two
@@ -718,33 +727,47 @@ cudaError_t launch_many(const Operands& o, const Epilogue& e, const LaunchCtx& c
 // How many clusters of `splits` CTAs of the few-token kernel the device holds at
 // once (a GPC takes whole clusters only: 90, 44 and 30 of 3, 6 and 8 here); asks
 // the runtime once. Its answer counts one CTA per SM, of two.
-int active_clusters(const void* kernel, int smem, int splits, int num_sms)
+template <int BN, bool E4M3, typename O>
+int active_clusters(int splits, int num_sms)
 {
-    static std::mutex mu;
-    static std::map<std::tuple<const void*, int, int>, int> known;
+    static std::atomic<int> known[64][kMostSplits + 1];
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return num_sms;
-    std::lock_guard<std::mutex> lock(mu);
-    auto [at, fresh] = known.try_emplace({kernel, splits, dev}, 0);
-    if (!fresh) return at->second;
-    int n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return num_sms / splits;
+    int n = known[dev & 63][splits].load(std::memory_order_relaxed);
+    if (n) return n;
+    using F = Few<BN, false>;
+    auto* kernel = linear_few_kernel<BN, E4M3, O, false>;
+    static std::atomic<uint64_t> allowed{0};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(splits, 1024);
     cfg.blockDim = dim3(kFewThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = F::kSmem;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = splits;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (allow_smem(kernel, smem) != cudaSuccess ||
+    if (allow_smem(reinterpret_cast<const void*>(kernel), F::kSmem, allowed) != cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
         cudaGetLastError();
         n = std::max(1, num_sms / splits);
     }
     if (n * splits <= num_sms) n *= 2;
-    return at->second = n;
+    known[dev & 63][splits].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+template <int BN, bool E4M3, typename O>
+cudaError_t launch_few(const Operands& o, const Epilogue& e, int splits, const LaunchCtx& ctx)
+{
+    if constexpr (BN >= 64) {
+        const long long tiles = (long long)((e.N + 127) / 128) * ((e.M + BN - 1) / BN);
+        const int room = splits == 1 ? ctx.num_sms : active_clusters<BN, E4M3, O>(splits, ctx.num_sms) / 2;
+        if (tiles <= room && (o.axis.blocks() + splits - 1) / splits > Few<BN, false>::kStages)
+            return launch_few_as<BN, E4M3, O, true>(o, e, splits, ctx);
+    }
+    return launch_few_as<BN, E4M3, O, false>(o, e, splits, ctx);
 }
 
 int tokens_per_tile(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
@@ -753,7 +776,7 @@ int tokens_per_tile(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 :
 // 1 to 2048 tokens and five weight shapes from 1024 x 2048 to 10576 x 2560, bf16
 // and e4m3 (off by a tenth on most, by a quarter at worst). A pair's tile takes
 // 0.31 us a block of K at 256 channels, where tensor cores and L2 balance, and
-// 0.215 at 128, where L2 bounds it; 2.5 and 1.5 us for its ends, and 4 more where
+// 0.215 at 128, where L2 bounds it; 2.5 and 1.5 us for its ends, and 2 more where
 // its rows leave through shared memory. The few-token
 // kernel takes a launch and the join (5.2 to 8 us with the tokens), and the
 // largest of its chain of stages (0.3 us a block), its traffic from L2 at 15
@@ -762,7 +785,7 @@ float many_us(long long tm, int N, int BN, int kblocks, bool wide, int num_sms)
 {
     const long long tiles = tm * ((N + BN - 1) / BN), pairs = num_sms / 2;
     const float waves = (float)((tiles + pairs - 1) / pairs);
-    return 5.0f + waves * ((BN == 256 ? 0.31f * kblocks + 2.5f : 0.215f * kblocks + 1.5f) + (wide ? 0.0f : 4.0f));
+    return 5.0f + waves * ((BN == 256 ? 0.31f * kblocks + 2.5f : 0.215f * kblocks + 1.5f) + (wide ? 0.0f : 2.0f));
 }
 float few_us(int BN, long long tiles, int N, int kblocks, int splits, int num_sms)
 {
@@ -778,10 +801,9 @@ float few_us(int BN, long long tiles, int N, int kblocks, int splits, int num_sm
 template <int BN, bool E4M3, typename O>
 int few_splits(long long tiles, int N, int kblocks, int num_sms)
 {
-    const void* kernel = reinterpret_cast<const void*>(linear_few_kernel<BN, E4M3, O>);
     int best = 1;
     for (int s = 2; s <= std::min(kMostSplits, kblocks / 2); ++s) {
-        if (tiles * s > 2ll * num_sms || tiles > active_clusters(kernel, Few<BN>::kSmem, s, num_sms)) break;
+        if (tiles * s > 2ll * num_sms || tiles > active_clusters<BN, E4M3, O>(s, num_sms)) break;
         if (few_us(BN, tiles, N, kblocks, s, num_sms) < few_us(BN, tiles, N, kblocks, best, num_sms)) best = s;
     }
     return best;
@@ -819,7 +841,10 @@ cudaError_t run(const Operands& o, const Epilogue& e, const LaunchCtx& ctx)
             }
         }
     }
-    return many128 < many256 ? launch_many<128, E4M3, O, kSeg>(o, e, ctx) : launch_many<256, E4M3, O, kSeg>(o, e, ctx);
+    // sixteen warps that turn rows round have room for 8 channels at a time, 32 bytes
+    // of a row; the eight of the narrower tile for 32 (16384 x 10001 x 1024: 668 us
+    // against 454)
+    return many128 < many256 || (kSeg && !wide) ? launch_many<128, E4M3, O, kSeg>(o, e, ctx) : launch_many<256, E4M3, O, kSeg>(o, e, ctx);
 }
 
 int element_bytes(const LinearArgs& a) { return a.type == LinearType::e4m3 ? 1 : a.type == LinearType::bf16 ? 2 : 4; }
