@@ -68,6 +68,11 @@ struct Epilogue {
 // -0.8e-6 after 1024), and the segments are joined with rounded additions.
 constexpr int kFewThreads = 256, kMostSplits = 8;
 
+template <int V>
+struct Int {
+    static constexpr int value = V;
+};
+
 // DEEP: one CTA per SM with all of its shared memory, for calls of no more CTAs
 // than SMs, whose stages in flight then are what hides the latency of a load
 // (1003 x 1777 x 1000, 112 CTAs of 16 blocks: DEEP_NOTE).
@@ -218,61 +223,86 @@ linear_few_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
     }
     const uint32_t red_addr = smem_addr(red);
     const O* res = static_cast<const O*>(e.residual);
-#pragma unroll 1
-    for (int t = rank + warp * splits; t < tokens; t += (kFewThreads / 32) * splits) {
-        const int m = m0 + t;
-        const long long row = (long long)m * e.N;
-        Packed<O, 4> r;
-        float rs[4];
-        if (res) {
-            if (vec && n < e.N) r.load(res + row + n);
+    const int stride = (kFewThreads / 32) * splits;  // tokens between a warp's
+    // Joins PARTS parts (or fewer, in the order of the ranks) of TOKENS tokens: all
+    // of their loads are under way before the first is used.
+    auto join = [&](auto tokens_c, auto parts_c, int t0) {
+        constexpr int TOKENS = decltype(tokens_c)::value, PARTS = decltype(parts_c)::value;
+        float rs[TOKENS][4], sx[TOKENS], v[TOKENS][4];
+        float4 p[TOKENS][PARTS];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (vec) rs[j] = r.get(j);
-                else if (n + j * step < e.N) rs[j] = static_cast<float>(res[row + n + j * step]);
+        for (int i = 0; i < TOKENS; ++i) {
+            const int t = min(t0 + i * stride, tokens - 1);  // past the last: that one again
+            sx[i] = E4M3 ? __ldg(e.x_scale + m0 + t) : 1.0f;
+            if (res) {
+                const O* from = res + (long long)(m0 + t) * e.N + n;
+                Packed<O, 4> r;
+                r.zero();
+                if (vec && n < e.N) r.load(from);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    rs[i][j] = r.get(j);
+                    if (!vec && n + j * step < e.N) rs[i][j] = static_cast<float>(from[j * step]);
+                }
+            }
+            const uint32_t at = red_addr + (uint32_t)(t * 128 + (vec ? lane * 4 : lane)) * 4;
+#pragma unroll
+            for (int k = 0; k < PARTS; ++k) {
+                if (k >= splits) break;
+                const uint32_t from = PARTS > 1 ? map_rank(at, k) : at;
+                if (vec) p[i][k] = ld_cluster_f4(from);
+                else p[i][k] = make_float4(ld_cluster_f1(from), ld_cluster_f1(from + 128), ld_cluster_f1(from + 256),
+                                           ld_cluster_f1(from + 384));
             }
         }
-        // every part is under way before the first is added
-        float4 p[kMostSplits];
-        const uint32_t at = red_addr + (uint32_t)(t * 128 + (vec ? lane * 4 : lane)) * 4;
 #pragma unroll
-        for (int k = 0; k < kMostSplits; ++k) {
-            if (k >= splits) break;
-            const uint32_t from = splits > 1 ? map_rank(at, k) : at;
-            if (vec) p[k] = ld_cluster_f4(from);
-            else p[k] = make_float4(ld_cluster_f1(from), ld_cluster_f1(from + 128), ld_cluster_f1(from + 256),
-                                    ld_cluster_f1(from + 384));
-        }
-        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = 0; i < TOKENS; ++i) {
+            v[i][0] = p[i][0].x; v[i][1] = p[i][0].y; v[i][2] = p[i][0].z; v[i][3] = p[i][0].w;
 #pragma unroll
-        for (int k = 0; k < kMostSplits; ++k) {
-            if (k >= splits) break;
-            v[0] += p[k].x; v[1] += p[k].y; v[2] += p[k].z; v[3] += p[k].w;
-        }
-        const float sx = E4M3 ? __ldg(e.x_scale + m) : 1.0f;
+            for (int k = 1; k < PARTS; ++k) {
+                if (k >= splits) break;
+                v[i][0] += p[i][k].x; v[i][1] += p[i][k].y; v[i][2] += p[i][k].z; v[i][3] += p[i][k].w;
+            }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if constexpr (E4M3) v[j] = v[j] * sx * ws[j];
-            if (e.bias) v[j] += bias[j];
-        }
-        if (e.act != SSD_ACT_NONE) {
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (E4M3) v[i][j] = v[i][j] * sx[i] * ws[j];
+                v[i][j] += bias[j];
+            }
+            if (e.act != SSD_ACT_NONE) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = activate(v[j], e.act);
-        }
-        if (res) {
+                for (int j = 0; j < 4; ++j) v[i][j] = activate(v[i][j], e.act);
+            }
+            if (res) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] += rs[j];
-        }
-        O* y = static_cast<O*>(e.y) + row + n;
-        if (vec) {
-            Packed<O, 4> out;
-            out.set(v);
-            if (n < e.N) out.store(y);
-        } else {
+                for (int j = 0; j < 4; ++j) v[i][j] += rs[i][j];
+            }
+            const int t = t0 + i * stride;
+            if (t >= tokens) break;
+            O* y = static_cast<O*>(e.y) + (long long)(m0 + t) * e.N + n;
+            if (vec) {
+                Packed<O, 4> out;
+                out.set(v[i]);
+                if (n < e.N) out.store(y);
+            } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (n + j * step < e.N) io<O>::store(y + j * step, v[j]);
+                for (int j = 0; j < 4; ++j)
+                    if (n + j * step < e.N) io<O>::store(y + j * step, v[i][j]);
+            }
         }
+    };
+    int t = rank + warp * splits;
+    if (splits == 1) {
+#pragma unroll 1
+        for (; t < tokens; t += 4 * stride) join(Int<4>{}, Int<1>{}, t);
+    } else if (splits == 2) {
+#pragma unroll 1
+        for (; t < tokens; t += 4 * stride) join(Int<4>{}, Int<2>{}, t);
+    } else if (splits <= 4) {
+#pragma unroll 1
+        for (; t < tokens; t += 2 * stride) join(Int<2>{}, Int<4>{}, t);
+    } else {
+#pragma unroll 1
+        for (; t < tokens; t += stride) join(Int<1>{}, Int<kMostSplits>{}, t);
     }
     if (splits > 1) cluster_sync();  // no CTA leaves while another reads its tile
 }
@@ -778,9 +808,10 @@ int tokens_per_tile(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 :
 // 0.31 us a block of K at 256 channels, where tensor cores and L2 balance, and
 // 0.215 at 128, where L2 bounds it; 2.5 and 1.5 us for its ends, and 2 more where
 // its rows leave through shared memory. The few-token
-// kernel takes a launch and the join (5.2 to 8 us with the tokens), and the
-// largest of its chain of stages (0.3 us a block), its traffic from L2 at 15
-// TB/s and the weights from HBM at 6 TB/s.
+// kernel takes 3.4 to 4.7 us for its ends with the tokens, 0.5 to 2 more where parts
+// of K are joined, and the largest of its chain of stages (0.28 us a block), its
+// traffic from L2 at 15 TB/s and the weights from HBM at 6 TB/s, with some of the
+// other two.
 float many_us(long long tm, int N, int BN, int kblocks, bool wide, int num_sms)
 {
     const long long tiles = tm * ((N + BN - 1) / BN), pairs = num_sms / 2;
@@ -790,10 +821,12 @@ float many_us(long long tm, int N, int BN, int kblocks, bool wide, int num_sms)
 float few_us(int BN, long long tiles, int N, int kblocks, int splits, int num_sms)
 {
     const float waves = (float)((tiles * splits + 2ll * num_sms - 1) / (2ll * num_sms));
-    const float chain = waves * 0.3f * ((kblocks + splits - 1) / splits);
+    const float chain = waves * 0.28f * ((kblocks + splits - 1) / splits);
     const float traffic = (float)tiles * kblocks * (128 + BN) * kRowBytes / 15e6f;
     const float weights = (float)N * kblocks * kRowBytes / 6e6f;
-    return waves * (4.8f + 0.025f * BN) + std::max(chain, std::max(traffic, weights));
+    const float ends = 3.2f + 0.012f * BN + (splits > 1 ? 0.3f + 0.012f * BN + 0.1f * splits : 0.0f);
+    const float longest = std::max(chain, std::max(traffic, weights));
+    return waves * ends + 0.85f * longest + 0.15f * (chain + traffic + weights);
 }
 
 // The parts of K of a call of the few-token kernel: the fewest of the shortest
