@@ -59,14 +59,20 @@ struct Epilogue {
 
 // ------------------------------------------------------------- few tokens
 
-// One CTA: 128 channels x BN tokens over its part of K. The parts of a cluster
-// meet in shared memory: every CTA writes its fp32 tile there, and CTA r adds up
-// the tokens r, r + S, ... in the order of the ranks, so the sum does not depend
-// on who is first. Within a CTA the K axis is cut again into segments with an
-// accumulator each: the tensor cores truncate each addition, a bias that grows
-// with the additions in a row (-4.7e-6 of the result after 5120 bf16 products,
-// -0.8e-6 after 1024), and the segments are joined with rounded additions.
-constexpr int kFewThreads = 256, kMostSplits = 8, kPrefetch = 6;
+// The tensor cores truncate each addition to an accumulator, a bias that grows with
+// the additions in a row: -4.7e-6 of the result after 5120 bf16 products, -0.8e-6
+// after 1024. fp32 outputs of bf16 operands are therefore summed in segments of
+// kSegBlocks blocks of K (768 products), joined in registers with rounded additions.
+// A bf16 output's own rounding hides the bias, and products of e4m3 values, with
+// eight significant bits at most, lose next to nothing (1e-8 at K = 5120).
+constexpr int kSegBlocks = 12;
+
+// One CTA: 128 channels x BN tokens over its part of K; eight warps that read the
+// accumulators (two, in turn, when there are several segments), one that loads and
+// one that issues the products. The parts of a cluster meet in shared memory: every
+// CTA writes its fp32 tile there, and CTA r adds up the tokens r, r + S, ... in the
+// order of the ranks, so the sum does not depend on who is first.
+constexpr int kFewWarps = 8, kFewThreads = 32 * (kFewWarps + 2), kMostSplits = 8, kPrefetch = 6;
 
 template <int V>
 struct Int {
@@ -84,7 +90,6 @@ struct Few {
     static constexpr int kRedBytes = BN * 128 * 4;
     static constexpr int kData = std::max(kStages * kStageBytes, kRedBytes);
     static constexpr int kSmem = 1024 + kData + 256;
-    static constexpr int kMaxSegments = BN >= 128 ? 2 : 4;
 };
 
 template <int BN, bool E4M3, typename O, bool DEEP>
@@ -103,8 +108,10 @@ linear_few_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(sm + F::kData);
     uint64_t* empty = full + NS;
-    uint64_t* done = empty + NS;
-    uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(done + 1);
+    uint64_t* acc_full = empty + NS;
+    uint64_t* acc_empty = acc_full + 2;
+    uint64_t* drained = acc_empty + 2;  // abort mode: every product issued has completed
+    uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(drained + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_ptr + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int splits = gridDim.x;
@@ -119,11 +126,15 @@ linear_few_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
             mbar_init(full + i, 1);
             mbar_init(empty + i, 1);
         }
-        mbar_init(done, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(acc_full + i, 1);
+            mbar_init(acc_empty + i, kFewWarps);
+        }
+        mbar_init(drained, 1);
         mbar_fence_init();
         *abort_flag = 0;
     }
-    if (warp == 1) {
+    if (warp == kFewWarps + 1) {
         tmem_alloc(tmem_ptr, tmem_cols);
         tmem_relinquish();
     }
@@ -148,7 +159,9 @@ linear_few_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
     wait_for_previous();
     let_next_begin();
 
-    if (warp == 0) {
+    const int tokens = min(BN, e.M - m0);
+    float* red = reinterpret_cast<float*>(sm);
+    if (warp == kFewWarps) {
         if (elect_one_sync()) {
             int issued = 0, section = kb0 / axis.per, block = kb0 - section * axis.per;
             for (; issued < count; ++issued) {
@@ -165,54 +178,72 @@ linear_few_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
                     ++section;
                 }
             }
-            // loads in flight end before the CTA does (in abort mode the MMA warp
+            // loads in flight end before the CTA does (in abort mode the products
             // may not have waited for them)
-            for (int i = std::max(0, issued - NS); i < issued; ++i)
+            for (int i = max(0, issued - NS); i < issued; ++i)
                 mbar_wait(full + i % NS, (i / NS) & 1, kPollLimit);
         }
-    } else if (warp == 1) {
+    } else if (warp == kFewWarps + 1) {
         if (elect_one_sync()) {
             constexpr uint32_t idesc = E4M3 ? idesc_e4m3(128, BN) : idesc_bf16(128, BN, false, false);
+            int unit = 0, r = 0;  // the segment and the block within it
             for (int i = 0; i < count; ++i) {
-                const int st = i % NS;
+                const int st = i % NS, buf = unit & 1;
+                if (r == 0 && unit >= 2) wait_or_abort(acc_empty + buf, ((unit >> 1) - 1) & 1, abort_flag, status);
                 wait_or_abort(full + st, (i / NS) & 1, abort_flag, status);
                 if (*abort_flag) break;
                 tc_fence_after_sync();
                 const uint32_t a = smem_addr(sm + st * F::kStageBytes);
                 const uint64_t ad = sdesc_sw128(a, 16, 1024), bd = sdesc_sw128(a + 128 * kRowBytes, 16, 1024);
-                const uint32_t d = tmem + (uint32_t)(i / seg_blocks) * BN;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    mma_step<E4M3, false>(d, ad + 2 * j, bd + 2 * j, idesc, i % seg_blocks != 0 || j != 0);
+                    mma_step<E4M3, false>(tmem + (uint32_t)buf * BN, ad + 2 * j, bd + 2 * j, idesc, r != 0 || j != 0);
                 mma_commit(empty + st);
+                if (++r == seg_blocks || i == count - 1) {
+                    mma_commit(acc_full + buf);
+                    ++unit;
+                    r = 0;
+                }
             }
-            mma_commit(done);
+            if (*abort_flag) {
+                mma_commit(drained);
+                mbar_wait(drained, 0, kPollLimit);
+            }
+        }
+    } else {
+        // warps 0..3 and 4..7 take a lane quadrant (32 channels) each, every other
+        // 16 tokens
+        constexpr int kChunks = BN >= 32 ? BN / 32 : 1;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const int units = (count + seg_blocks - 1) / seg_blocks, c0 = (warp >> 2) * 16;
+        float sum[kChunks * 16];
+        for (int u = 0; u < units; ++u) {
+            const int buf = u & 1;
+            wait_or_abort(acc_full + buf, (u >> 1) & 1, abort_flag, status);
+            tc_fence_after_sync();
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+                if (c0 + 32 * i >= tokens) break;
+                uint32_t v[16];
+                tmem_ld16_sync(lanes + buf * BN + c0 + 32 * i, v);
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    sum[16 * i + j] = u == 0 ? __uint_as_float(v[j]) : sum[16 * i + j] + __uint_as_float(v[j]);
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_empty + buf);
+        }
+        // into shared memory as [token][channel]: the last accumulator is full, so
+        // every product has read its stages and their memory is free
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            if (c0 + 32 * i >= tokens) break;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) red[(c0 + 32 * i + j) * 128 + (warp & 3) * 32 + lane] = sum[16 * i + j];
         }
     }
     __syncwarp();
-    wait_or_abort(done, 0, abort_flag, status);
-    tc_fence_after_sync();
-    // this CTA's tile: lane = channel; into shared memory as [token][channel].
-    // Every MMA has read its stages by now, so the stages' memory is free.
-    float* red = reinterpret_cast<float*>(sm);
-    const int segments = (count + seg_blocks - 1) / seg_blocks;
-    // warps 0..3 and 4..7 take a lane quadrant each, every other 16 tokens
-    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const int tokens = min(BN, e.M - m0);
-#pragma unroll 1
-    for (int c = (warp >> 2) * 16; c < tokens; c += 32) {
-        uint32_t v[16];
-        tmem_ld16_sync(lanes + c, v);
-        for (int s = 1; s < segments; ++s) {
-            uint32_t u[16];
-            tmem_ld16_sync(lanes + s * BN + c, u);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(u[j]));
-        }
-#pragma unroll
-        for (int j = 0; j < 16; ++j) red[(c + j) * 128 + (warp & 3) * 32 + lane] = __uint_as_float(v[j]);
-    }
-    tc_fence_before_sync();
 
     // this thread's four channels of every token it joins: neighbours where rows
     // of y and residual start on four elements, else a warp's width apart
@@ -227,13 +258,13 @@ linear_few_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
     }
     if (splits > 1) cluster_sync();
     else __syncthreads();
-    if (warp == 1) {
+    if (warp == kFewWarps + 1) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, tmem_cols);
     }
     const uint32_t red_addr = smem_addr(red);
     const O* res = static_cast<const O*>(e.residual);
-    const int stride = (kFewThreads / 32) * splits;  // tokens between a warp's
+    const int stride = kFewWarps * splits;  // tokens between a warp's
     // Joins PARTS parts (or fewer, in the order of the ranks) of TOKENS tokens: all
     // of their loads are under way before the first is used.
     auto join = [&](auto tokens_c, auto parts_c, int t0) {
@@ -300,7 +331,7 @@ linear_few_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
             }
         }
     };
-    int t = rank + warp * splits;
+    int t = warp < kFewWarps ? rank + warp * splits : tokens;
     if (splits == 1) {
 #pragma unroll 1
         for (; t < tokens; t += 4 * stride) join(Int<4>{}, Int<1>{}, t);
@@ -325,11 +356,8 @@ cudaError_t launch_few_as(const Operands& o, const Epilogue& e, int splits, cons
     const int kblocks = o.axis.blocks();
     const int tn = (e.N + 127) / 128, tm = (e.M + BN - 1) / BN;
     const int per = (kblocks + splits - 1) / splits;  // blocks of the longest part
-    // about 512 bf16 products to a segment, as far as the accumulators go
-    const int seg_blocks = std::max(8, (per + F::kMaxSegments - 1) / F::kMaxSegments);
-    const int segments = (per + seg_blocks - 1) / seg_blocks;
-    uint32_t cols = 32;
-    while ((int)cols < segments * BN) cols *= 2;
+    const int seg_blocks = sizeof(O) == 4 && !E4M3 ? kSegBlocks : per;
+    const uint32_t cols = std::max(32, seg_blocks < per ? 2 * BN : BN);
     CUtensorMap wmap, xmap;
     if (!make_map_rows(&wmap, o.w, E4M3, o.w_cols, e.N, o.w_pitch * es, 128) ||
         !make_map_rows(&xmap, o.x, E4M3, o.x_cols, e.M, o.x_pitch * es, BN))
@@ -351,11 +379,8 @@ cudaError_t launch_few_as(const Operands& o, const Epilogue& e, int splits, cons
 // (128 lanes = tokens, BN columns in each CTA) take turns in TMEM, so the
 // epilogue of one runs under the products of the next.
 //
-// SEG (fp32 outputs of bf16 operands): the epilogue warps hold the tile in registers and add up
-// accumulators of at most kSegBlocks K blocks (768 products) with rounded additions, against
-// the bias of the tensor cores' truncated ones (see linear_few_kernel). A bf16
-// output's own rounding hides that bias, and products of e4m3 values, with eight
-// significant bits at most, lose next to nothing (measured 1e-8 at K = 5120).
+// SEG (fp32 outputs of bf16 operands): the epilogue warps hold the tile in registers
+// and join its segments there (see kSegBlocks).
 template <int BN, bool SEG>
 struct Many {
     static constexpr int kBRows = BN / 2;
@@ -373,7 +398,6 @@ struct Many {
     static constexpr int kTurnBytes = 32 * (kTurn + 1) * 4 * kEpiWarps;
     static constexpr int kSmem = 1024 + kStages * kStageBytes + kTurnBytes + 512;
     static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
-    static constexpr int kSegBlocks = 12;
 };
 
 // 32 bytes of one row (rows that allow it start on 32 bytes).
@@ -549,7 +573,7 @@ linear_many_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     const int kblocks = axis.blocks();
-    const int seg = SEG ? T::kSegBlocks : kblocks;  // K blocks of one accumulator
+    const int seg = SEG ? kSegBlocks : kblocks;  // K blocks of one accumulator
     const int segs = SEG ? (kblocks + seg - 1) / seg : 1;
 
     if (threadIdx.x == 0) {
