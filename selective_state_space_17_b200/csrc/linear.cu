@@ -81,7 +81,7 @@ struct Int {
 
 // DEEP: one CTA per SM with all of its shared memory, for calls of no more CTAs
 // than SMs, whose stages in flight then are what hides the latency of a load
-// (1003 x 1777 x 1000, 112 CTAs of 16 blocks: DEEP_NOTE).
+// (1003 x 1777 x 1000, 112 CTAs of 16 blocks: 12.0 us against 13.6).
 template <int BN, bool DEEP>
 struct Few {
     static constexpr int kStageBytes = 128 * kRowBytes + BN * kRowBytes;
@@ -929,7 +929,9 @@ enum class Path { direct, pack, split, rows, simt };
 
 // Operands that the tensor cores take as they lie go there. The others pay for
 // another copy of the weights, worth it from so many tokens on that the rows
-// kernel, which reads them as they are, is bound by its FMAs (ROWS_NOTE).
+// kernel, which reads them as they are and bounded by its FMAs by then, has lost
+// (2560 x 2560 in fp32: 37 us for 32 tokens as they are, 43 for 33 with copies;
+// 2560 x 2561 in bf16: 26 us for 16, 24 for 17).
 Path path_of(const LinearArgs& a)
 {
     if (g_variant == 1) return Path::simt;
