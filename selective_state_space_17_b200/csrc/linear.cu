@@ -452,7 +452,7 @@ __device__ __forceinline__ void store_row(const Epilogue& e, const void* residua
 #pragma unroll
         for (int j = 0; j < CH; ++j) v[j] = silu_f(v[j]);
     } else if (e.act == SSD_ACT_GELU) {
-        // rolled for the sake of erfc's length; rotating the values by 8 keeps
+        // rolled for the sake of the code's length; rotating the values by 8 keeps
         // their indexes constants
 #pragma unroll 1
         for (int c = 0; c < CH; c += 8) {
