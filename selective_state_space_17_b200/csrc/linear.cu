@@ -12,6 +12,11 @@
 // Both stage operand rows of 128 bytes (64 bf16 or 128 e4m3 values) by TMA with
 // the 128-byte swizzle; one tcgen05.mma takes 32 bytes of each row, whatever
 // the type, so the two types share all but the instruction.
+//
+// Measured (channels x K): 64 tokens, 10576 x 2560, bf16 14.5 us (55 MB of weights:
+// 3.8 TB/s), e4m3 10 us; one token, 1024 x 2048, 4.2 us; 16384 tokens, 10576 x 2560,
+// in bursts bf16 600 us (1480 TFLOP/s) and e4m3 336 us (2640), in a long loop under
+// the power cap 686 and 376 us; 2560 x 5120 with an fp32 residual 361 us (1190).
 #include <algorithm>
 #include <atomic>
 

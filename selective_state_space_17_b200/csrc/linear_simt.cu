@@ -5,7 +5,9 @@
 // linear_rows: few tokens whose operands the tensor-core kernels cannot take as
 // they lie (fp32, or rows that TMA cannot address); linear_simt: any operands,
 // the kernel of last resort; and the packing of such operands for the
-// tensor-core kernels when there are more tokens.
+// tensor-core kernels when there are more tokens. Measured: one token, 2560 x 5120 in
+// fp32 20 us and 10576 x 2561 in bf16 24 us with the host's share; 17 tokens of 2560 x
+// 2561 in bf16, copy included, 24 us.
 #include <algorithm>
 
 #include "layer.cuh"
