@@ -256,13 +256,14 @@ def linear(x, w, bias=None, activation: str = "none", residual=None, x_scale=Non
 
 
 def _conv_weights(weight, bias, dt, dt_bias, C, H, dev):
-    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+    if not isinstance(weight, _Tensor) or weight.dim() != 2:
         raise ValueError("weight must be [C, width]")
     if dt is None and dt_bias is not None:
         raise ValueError("dt_bias needs dt")
     W = weight.shape[1]
-    return (W, _arg(weight, "weight", _F32, dev, (C, W)), _arg(bias, "bias", _F32, dev, (C,)),
-            _arg(dt_bias, "dt_bias", _F32, dev, (H,)))
+    return (W, _arg(weight, "weight", _F32, dev, (C, W)),
+            None if bias is None else _arg(bias, "bias", _F32, dev, (C,)),
+            None if dt_bias is None else _arg(dt_bias, "dt_bias", _F32, dev, (H,)))
 
 
 def _conv_activation(activation):
