@@ -11,8 +11,8 @@
 // loads in flight, so a strip reads its tokens and W - 1 more; neighbouring
 // strips run at about the same time, and their overlap hits L2. What counts is the
 // bytes in flight: four channels to a thread (8 bytes of bf16) and each token's
-// load eight tokens before its use measured 71.5 us at 4 x 4096 x 5376 in bf16,
-// 5.0 TB/s, four tokens ahead 82 us, and eight channels with four tokens loaded
+// load eight tokens before its use measured 70 us at 4 x 4096 x 5376 in bf16,
+// 5.1 TB/s, four tokens ahead 82 us, and eight channels with four tokens loaded
 // before each four 118 us at 127 registers a thread. The exponentials and
 // reciprocals of SiLU take 40 us of the special-function unit meanwhile. The
 // single-token form is the same kernel with one token per strip; it may shift the
@@ -44,14 +44,36 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && VEC > 1 && kAhead 
     if ((int)blockIdx.x >= channel_ctas) {
         // step sizes of this strip's tokens
         const T* raw = static_cast<const T*>(a.dt_raw) + b * a.dt_batch;
-        // a warp to a token, its lanes along the heads
-        const int warps = ((int)gridDim.x - channel_ctas) * (kThreads / 32);
-        for (int t = t0 + (((int)blockIdx.x - channel_ctas) * kThreads + threadIdx.x) / 32; t < t1; t += warps)
-            for (int h = threadIdx.x & 31; h < a.H; h += 32) {
-                float v = io<T>::load(raw + t * a.dt_row + h);
-                if (a.dt_bias) v += __ldg(a.dt_bias + h);
-                a.dt[((long long)b * a.L + t) * a.H + h] = softplus_f(v);
+        // (t, h) steps by the CTAs' threads: q tokens and r heads; kBatch loads are
+        // under way before the first is used
+        constexpr int kBatch = 4;
+        const int threads = ((int)gridDim.x - channel_ctas) * kThreads;
+        const int first = ((int)blockIdx.x - channel_ctas) * kThreads + threadIdx.x;
+        const int q = threads / a.H, r = threads - q * a.H;
+        int t = t0 + first / a.H, h = first % a.H;
+        while (t < t1) {
+            T in[kBatch];
+            int ts[kBatch], hs[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                ts[i] = t;
+                hs[i] = h;
+                if (t < t1) in[i] = raw[t * a.dt_row + h];
+                t += q;
+                h += r;
+                if (h >= a.H) {
+                    h -= a.H;
+                    ++t;
+                }
             }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                if (ts[i] >= t1) break;
+                float v = static_cast<float>(in[i]);
+                if (a.dt_bias) v += __ldg(a.dt_bias + hs[i]);
+                a.dt[((long long)b * a.L + ts[i]) * a.H + hs[i]] = softplus_f(v);
+            }
+        }
         return;
     }
     const int C = a.C();
@@ -164,7 +186,7 @@ cudaError_t launch(const ConvArgs& a, const LaunchCtx& ctx)
     strip = std::max(strip, a.L / 65535 + 1);  // the grid's y extent
     strip = (strip + kAhead - 1) / kAhead * kAhead;
     const int strips = (a.L + strip - 1) / strip;
-    const int dx = a.dt_raw ? std::max(1, std::min(std::min(strip, a.L) / (kThreads / 32), 2)) : 0;
+    const int dx = a.dt_raw ? std::max(1, std::min(a.H / 256, 8)) : 0;  // CTAs of a strip's step sizes
     return launch_overlapped(conv_kernel<T, VEC, W, kAhead>, dim3(cx + dx, strips, a.B), kThreads, 0, ctx.stream, 1, a,
                              strip, cx);
 }
