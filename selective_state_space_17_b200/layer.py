@@ -43,7 +43,8 @@ _OPERAND = {_F32: SSD_F32, _BF16: SSD_BF16, _E4M3: SSD_E4M3}
 
 
 # The current device and stream as plain numbers: these calls stand in front of
-# every launch, and the ones that build Stream objects take 2 us.
+# every launch, and the ones that build Stream objects take 2 us. (Likewise
+# new_empty takes its sizes as arguments below: a tuple costs it 0.4 us more.)
 _device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
@@ -170,7 +171,7 @@ def rms_norm(x, weight, residual=None, gate=None, eps: float = 1e-5, groups: int
         if y is None:
             y = torch.empty_like(x, dtype=_E4M3)
         if scale is None:
-            scale = x.new_empty(shape[:-1], dtype=_F32)
+            scale = x.new_empty(*shape[:-1], dtype=_F32) if len(shape) > 1 else x.new_empty((), dtype=_F32)
         py = _arg(y, "y", _E4M3, dev, shape)
         ps = _arg(scale, "scale", _F32, dev, shape[:-1])
     else:
@@ -228,7 +229,7 @@ def linear(x, w, bias=None, activation: str = "none", residual=None, x_scale=Non
         raise TypeError(f"output dtype must be bfloat16 or float32, got {out_dtype}")
     shape = (*lead, N)
     if y is None:
-        y = x.new_empty(shape, dtype=out_dtype)
+        y = x.new_empty(*shape, dtype=out_dtype)
         py = y.data_ptr()
     else:
         py = _arg(y, "y", out_dtype, dev, shape)
@@ -299,19 +300,19 @@ def conv(u, weight, bias, H: int, P: int, G: int, N: int, dt=None, dt_bias=None,
     pu = _strided(u, "u", dtype, dev, u.shape)
     W, pw, pb, pdb = _conv_weights(weight, bias, dt, dt_bias, C, H, dev)
     act = _conv_activation(activation)
-    x = u.new_empty((B, L, H, P))
-    Bm = u.new_empty((B, L, G, N))
+    x = u.new_empty(B, L, H, P)
+    Bm = u.new_empty(B, L, G, N)
     Cm = torch.empty_like(Bm)
     out = pdt = po = None
     db = dr = 0
     if dt is not None:
         pdt = _strided(dt, "dt", dtype, dev, (B, L, H))
         db, dr, _ = dt.stride()
-        out = u.new_empty((B, L, H), dtype=_F32)
+        out = u.new_empty(B, L, H, dtype=_F32)
         po = out.data_ptr()
     state_shape = (B, W - 1, C)
     if final_state is None and return_final_state:
-        final_state = u.new_empty(state_shape)
+        final_state = u.new_empty(*state_shape)
     ub, ur, _ = u.stride()
     rc = lib.ssd_conv(pu, ub, ur, pw, pb, pdt, db, dr, pdb,
                       _arg(initial_state, "initial_state", dtype, dev, state_shape), x.data_ptr(),
@@ -345,15 +346,15 @@ def conv_step(u, weight, bias, state, H: int, P: int, G: int, N: int, dt=None, d
     if state is None:
         raise ValueError("state is required")
     ps = _arg(state, "state", dtype, dev, (B, W - 1, C))
-    x = u.new_empty((B, H, P))
-    Bm = u.new_empty((B, G, N))
+    x = u.new_empty(B, H, P)
+    Bm = u.new_empty(B, G, N)
     Cm = torch.empty_like(Bm)
     out = pdt = po = None
     dr = 0
     if dt is not None:
         pdt = _strided(dt, "dt", dtype, dev, (B, H))
         dr = dt.stride(0)
-        out = u.new_empty((B, H), dtype=_F32)
+        out = u.new_empty(B, H, dtype=_F32)
         po = out.data_ptr()
     rc = lib.ssd_conv_step(pu, u.stride(0), pw, pb, pdt, dr, pdb, ps, x.data_ptr(), Bm.data_ptr(),
                            Cm.data_ptr(), po, B, H, P, G, N, W, act, code, _raw_stream(dev))
