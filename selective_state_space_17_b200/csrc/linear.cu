@@ -933,16 +933,20 @@ bool w_addressable(const LinearArgs& a) { return (long long)a.K * element_bytes(
 enum class Path { direct, pack, split, rows, simt };
 
 // Operands that the tensor cores take as they lie go there. The others pay for
-// another copy of the weights, worth it from so many tokens on that the rows
-// kernel, which reads them as they are and bounded by its FMAs by then, has lost
-// (2560 x 2560 in fp32: 37 us for 32 tokens as they are, 43 for 33 with copies;
-// 2560 x 2561 in bf16: 26 us for 16, 24 for 17).
+// another copy of the weights, or, for a few tokens, are read as they lie by the rows
+// kernel: whichever takes less by these estimates, fitted to 1 to 32 tokens of 300 x
+// 700 to 10576 x 2561 (microseconds; the copies' own launches are their constants).
 Path path_of(const LinearArgs& a)
 {
     if (g_variant == 1) return Path::simt;
-    if (a.type != LinearType::f32 && x_addressable(a) && w_addressable(a)) return Path::direct;
-    if (g_variant == 0 && a.M <= (a.type == LinearType::f32 ? 32 : 16)) return Path::rows;
-    return a.type == LinearType::f32 ? Path::split : Path::pack;
+    const bool f32 = a.type == LinearType::f32, addressable = x_addressable(a) && w_addressable(a);
+    if (!f32 && addressable) return Path::direct;
+    const float nk = 1e-6f * a.N * a.K;
+    const float each = addressable || (a.type == LinearType::e4m3 && a.M == 1) ? 0.65f : 1.4f;
+    const float rows = 2.0f + nk * std::max(each, 0.27f * a.M);
+    const float copies = f32 ? 12.0f + 3.5f * nk : 8.0f + 1.15f * nk;
+    if (g_variant == 0 && a.M <= (f32 ? 32 : 16) && rows <= copies) return Path::rows;
+    return f32 ? Path::split : Path::pack;
 }
 
 // Workspace: a flag (256 bytes), then x's copy, then w's.

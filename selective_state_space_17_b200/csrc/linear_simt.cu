@@ -81,26 +81,26 @@ __global__ void __launch_bounds__(256) linear_simt_kernel(LinearArgs a, const un
     }
 }
 
-// MT tokens x kCh channels per CTA: its warps take every eighth piece of 32 * VEC
+// MT tokens x CH channels per CTA: its warps take every eighth piece of 32 * VEC
 // of the K axis, so the weights are read once, in whole lines, and a call with
 // few channels still has many loads in flight; the lanes' and the warps' parts
 // are added up in a fixed order. Bound by the weights' bytes.
-constexpr int kCh = 4, kRowWarps = 8;
+constexpr int kRowWarps = 8;
 
-template <typename T, typename O, int MT, int VEC>
+template <typename T, typename O, int MT, int CH, int VEC>
 __global__ void __launch_bounds__(32 * kRowWarps) linear_rows_kernel(LinearArgs a)
 {
-    __shared__ float part[kRowWarps][MT * kCh];
+    __shared__ float part[kRowWarps][MT * CH];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int n0 = blockIdx.x * kCh, m0 = blockIdx.y * MT;
+    const int n0 = blockIdx.x * CH, m0 = blockIdx.y * MT;
     const T* x = static_cast<const T*>(a.x);
     const T* w = static_cast<const T*>(a.w);
-    float acc[MT][kCh] = {};
+    float acc[MT][CH] = {};
 #pragma unroll(MT > 4 ? 2 : 4)
     for (int k = (warp * 32 + lane) * VEC; k < a.K; k += 32 * kRowWarps * VEC) {
-        float wv[kCh][VEC];
+        float wv[CH][VEC];
 #pragma unroll
-        for (int c = 0; c < kCh; ++c) {
+        for (int c = 0; c < CH; ++c) {
             const T* p = w + (long long)min(n0 + c, a.N - 1) * a.K + k;
             if constexpr (VEC > 1) {
                 const float4 f = __ldg(reinterpret_cast<const float4*>(p));
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) linear_rows_kernel(LinearArgs 
                 xv[0] = load_as_f32(p);
             }
 #pragma unroll
-            for (int c = 0; c < kCh; ++c)
+            for (int c = 0; c < CH; ++c)
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) acc[i][c] = fmaf(xv[j], wv[c][j], acc[i][c]);
         }
@@ -128,14 +128,14 @@ __global__ void __launch_bounds__(32 * kRowWarps) linear_rows_kernel(LinearArgs 
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int c = 0; c < kCh; ++c) {
+        for (int c = 0; c < CH; ++c) {
 #pragma unroll
             for (int o = 16; o; o >>= 1) acc[i][c] += __shfl_xor_sync(0xffffffffu, acc[i][c], o);
-            if (lane == 0) part[warp][i * kCh + c] = acc[i][c];
+            if (lane == 0) part[warp][i * CH + c] = acc[i][c];
         }
     __syncthreads();
-    if (threadIdx.x < MT * kCh) {
-        const int m = m0 + threadIdx.x / kCh, n = n0 + threadIdx.x % kCh;
+    if (threadIdx.x < MT * CH) {
+        const int m = m0 + threadIdx.x / CH, n = n0 + threadIdx.x % CH;
         float v = 0.0f;
 #pragma unroll
         for (int k = 0; k < kRowWarps; ++k) v += part[k][threadIdx.x];
@@ -146,11 +146,10 @@ __global__ void __launch_bounds__(32 * kRowWarps) linear_rows_kernel(LinearArgs 
 template <typename T, typename O, int VEC>
 cudaError_t launch_rows(const LinearArgs& a, const LaunchCtx& ctx)
 {
-    const unsigned cols = (a.N + kCh - 1) / kCh;
-    const auto grid = [&](int mt) { return dim3(cols, (a.M + mt - 1) / mt); };
-    if (a.M == 1) linear_rows_kernel<T, O, 1, VEC><<<grid(1), 32 * kRowWarps, 0, ctx.stream>>>(a);
-    else if (a.M <= 4) linear_rows_kernel<T, O, 4, VEC><<<grid(4), 32 * kRowWarps, 0, ctx.stream>>>(a);
-    else linear_rows_kernel<T, O, 8, VEC><<<grid(8), 32 * kRowWarps, 0, ctx.stream>>>(a);
+    const auto grid = [&](int mt, int ch) { return dim3((a.N + ch - 1) / ch, (a.M + mt - 1) / mt); };
+    if (a.M == 1) linear_rows_kernel<T, O, 1, 4, VEC><<<grid(1, 4), 32 * kRowWarps, 0, ctx.stream>>>(a);
+    else if (a.M <= 4) linear_rows_kernel<T, O, 4, 4, VEC><<<grid(4, 4), 32 * kRowWarps, 0, ctx.stream>>>(a);
+    else linear_rows_kernel<T, O, 8, 8, VEC><<<grid(8, 8), 32 * kRowWarps, 0, ctx.stream>>>(a);
     return cudaGetLastError();
 }
 
