@@ -250,8 +250,8 @@ ssd_status ssd_rms_norm(const void* x, const void* residual, const void* gate, i
  *             and e4m3 operands with rows of 16-byte multiples from a 16-byte
  *             base: those go to the tensor cores as they lie. Others are copied
  *             there first (fp32 as three bf16 parts, which keeps its 24 bits)
- *             unless reading a few tokens' worth as it lies takes less. It needs no clearing; calls
- *             ordered on one stream may share it.
+ *             unless reading a few tokens' worth as it lies takes less. It needs
+ *             no clearing; calls ordered on one stream may share it.
  *   Sizes: M, N >= 0 (0 is a no-op), K >= 1; M <= 2^30; N, K <= 2^20. x needs its
  *   element's alignment only; every other pointer is 16-byte aligned.
  *   The result does not depend on the path beyond rounding: bf16 products are

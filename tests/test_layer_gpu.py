@@ -101,7 +101,7 @@ def check_norm(ssd, x, weight, residual=None, gate=None, groups=1, eps=1e-5, qua
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("rows,D,groups", [
     (1, 1, 1), (3, 8, 1), (5, 7, 7), (1, 64, 1), (7, 256, 1), (9, 264, 1), (33, 1000, 1), (3, 1237, 1),
-    (17, 2560, 8), (2, 5120, 1), (600, 512, 4), (3, 10240, 32), (4, 4100, 1), (2, 16392, 1), (1, 20001, 3),
+    (17, 2560, 8), (2, 5120, 1), (600, 512, 4), (3, 10240, 32), (4, 4100, 1), (700, 5120, 8), (650, 2570, 1), (2500, 77, 1), (2, 16392, 1), (1, 20001, 3),
 ])
 def test_norm(ssd, rows, D, groups, dtype, mode, quantize):
     g = gen(rows * 31 + D)
