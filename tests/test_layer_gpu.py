@@ -728,3 +728,34 @@ def test_refusals_on_the_device(ssd):
         ssd.conv(u, cw, None, 2, 64, 1, 16, dt_bias=f[:2].contiguous())
     with pytest.raises(ValueError, match="state is required"):
         ssd.conv_step(u[:, 0], cw, None, None, 2, 64, 1, 16)
+
+
+def test_offsets_beyond_32_bits(ssd):
+    """The last rows of operands and outputs of more than 2^31 elements."""
+    g = gen(16)
+    M, D = 4_200_000, 512
+    x, w = randn(g, M, D, dtype=BF16), 1 + 0.1 * randn(g, D)
+    last = slice(M - 100, M)
+    y, s, _ = ssd.rms_norm(x, w, quantize=True)
+    _, want = norm64(x[last], w, None, None, 1e-5, 1)
+    check("norm", y[last].double() * s[last].double()[:, None], want,
+          want.abs() * (norm_rel(D, 1) + 8 * U + HALF[E4M3]) + s[last].double()[:, None] * E4M3_SUBNORMAL_HALF * 1.001)
+    del x, y
+    M, K = 2_000_000, 1088
+    x = randn(g, M, K, dtype=BF16)
+    for N in (1088, 1089):
+        w = randn(g, N, K, dtype=BF16, scale=0.03)
+        y = ssd.linear(x, w)
+        last = slice(M - 100, M)
+        want = x[last].double() @ w.double().t()
+        size = x[last].double().abs() @ w.double().abs().t()
+        check("linear", y[last], want, size * (2 * K + 8) * U + want.abs() * HALF[BF16] * 1.01)
+        del y
+    del x
+    L, sizes = 1_000_000, (32, 64, 1, 128)
+    C = 32 * 64 + 256
+    u, w = randn(g, 1, L, C, dtype=BF16), randn(g, C, 4, scale=0.5)
+    got = ssd.conv(u, w, None, *sizes)
+    tail = u[:, L - 40:]
+    c = dict(u=tail, weight=w)
+    check_conv(c, sizes, [t[:, L - 40:] for t in got[:3]] + [None, got[4]], u[:, L - 43:L - 40], bias=False)
