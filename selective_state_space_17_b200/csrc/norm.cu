@@ -175,8 +175,11 @@ __device__ __forceinline__ Factors join_row(float2 acc, const NormArgs& a, const
     if constexpr (!Q8) return {rho, 1.0f};
     const float amax = acc.y * rho;
     if (writer) a.scale[row] = max_nan(amax / kE4m3Max, kScaleMin);
-    // the smallest scale, NaN, or a maximum that the fast division takes for infinite
-    if (!(amax >= kE4m3Max * kScaleMin) || acc.y > 8e37f) return over_scale(rho, max_nan(amax / kE4m3Max, kScaleMin));
+    // the smallest scale, NaN, a maximum that the fast division takes for infinite, or
+    // one so small that 448 over it is (below 448 / 3.4e38 = 1.32e-36: rho may put its
+    // scale far above the smallest)
+    if (!(amax >= kE4m3Max * kScaleMin) || !(acc.y >= 1.4e-36f && acc.y <= 8e37f))
+        return over_scale(rho, max_nan(amax / kE4m3Max, kScaleMin));
     return {__fdividef(kE4m3Max, acc.y), 1.0f};
 }
 

@@ -1,0 +1,63 @@
+"""The operators around the SSD core at the values and widths that
+test_layer_gpu.py does not reach: rows of tiny values in 8 bits, groups of three
+vectors to a lane, and the precision of what is done in fp32 (the activations, the
+three bf16 parts of an fp32 operand, the segments of a long sum), each against the
+formula in 64 bits.
+
+Tolerances count roundings as in test_layer_gpu.py: U = 2^-24 of the result for one in
+fp32, 2^-149 absolute below its normal range.
+"""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from test_layer_gpu import (BF16, E4M3, E4M3_SUBNORMAL_HALF, F32, HALF, U, check, check_norm, gen, norm64,  # noqa: E402
+                            norm_rel, quantize_rows, randn)
+
+pytestmark = pytest.mark.gpu
+
+DENORMAL = 2.0 ** -149
+
+
+@pytest.fixture(scope="module")
+def ssd():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import selective_state_space_17_b200 as _ssd
+    return _ssd
+
+
+# ---------------------------------------------------------------- rms_norm
+
+@pytest.mark.parametrize("mode", ["plain", "residual", "gate"])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("D,groups,eps", [(64, 1, 1e-5), (97, 1, 1e-5), (4096, 1, 1e-5), (4096, 4, 1e-5), (40000, 1, 1e-5),
+                                          (512, 1, 1e-12), (512, 4, 1e-12)])
+def test_norm_of_tiny_rows_in_8_bits(ssd, D, groups, eps, dtype, mode):
+    """Rows from below the smallest scale's to above 448 / FLT_MAX, zeros among them,
+    in registers and read twice: what is stored times the scale is the formula's."""
+    g = gen(D + groups)
+    tops = torch.tensor([1e-39, 1e-38, 2e-38, 1e-37, 5e-37, 1e-36, 1.3e-36, 1.5e-36, 3e-36, 1e-35, 1e-30],
+                        device="cuda")
+    v = randn(g, len(tops), D)
+    v = v / v.abs().amax(-1, keepdim=True) * tops[:, None]
+    v[:, 3::7] = 0
+    kw = {}
+    if mode == "residual":
+        kw["residual"] = torch.zeros_like(v)
+    if mode == "gate":
+        kw["gate"] = torch.full((len(tops), D), 3.0, device="cuda", dtype=dtype)
+    x, weight = v.to(dtype), torch.ones(D, device="cuda")
+    q, s, _ = ssd.rms_norm(x, weight, eps=eps, groups=groups, quantize=True, **kw)
+    _, want = norm64(x, weight, kw.get("residual"), kw.get("gate"), eps, groups)
+    rel, rho = norm_rel(D, groups), eps ** -0.5
+    # v and v w may lie below fp32's normal range, each within half a step of it, and rho
+    # carries that to y; the scale is at least 2^-126, the end of that range
+    absolute = rho * DENORMAL
+    scale = (want.abs().amax(-1) / 448).clamp_min(2.0 ** -126)
+    check("scale", s, scale, scale * (rel + 2 * U) + absolute / 448)
+    check("y", q.double() * s.double()[:, None], want,
+          want.abs() * (rel + 8 * U + HALF[E4M3]) * (1 + 2.0 ** -20) + absolute
+          + s.double()[:, None] * E4M3_SUBNORMAL_HALF * 1.001)
