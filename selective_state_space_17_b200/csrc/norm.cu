@@ -396,6 +396,14 @@ cudaError_t launch(const NormArgs& a, const LaunchCtx& ctx)
     const long long cap = (long long)ctx.num_sms * std::max(1, 1024 / threads);
     const unsigned grid = (unsigned)std::min(ctas, cap);
     const size_t smem = shared_weights(MODE, VPT * VEC) ? sizeof(float) * VPT * VEC * threads : 0;
+    // three vectors of 8 to each of 512 threads are 48 KB beside the reduction's 512
+    // bytes: more than a kernel gets without asking
+    if constexpr (shared_weights(MODE, VPT * VEC) && VPT == 3) {
+        static std::atomic<uint64_t> allowed{0};
+        const cudaError_t err = allow_smem(reinterpret_cast<const void*>(rms_norm_kernel<T, R, MODE, Q8, VEC, VPT>),
+                                           (int)sizeof(float) * VPT * VEC * 512, allowed);
+        if (err != cudaSuccess) return err;
+    }
     if constexpr (VPT > 0)
         return launch_overlapped(rms_norm_kernel<T, R, MODE, Q8, VEC, VPT>, grid, threads, smem, ctx.stream, 1, a, wpg);
     else

@@ -61,3 +61,20 @@ def test_norm_of_tiny_rows_in_8_bits(ssd, D, groups, eps, dtype, mode):
     check("y", q.double() * s.double()[:, None], want,
           want.abs() * (rel + 8 * U + HALF[E4M3]) * (1 + 2.0 ** -20) + absolute
           + s.double()[:, None] * E4M3_SUBNORMAL_HALF * 1.001)
+
+
+@pytest.mark.parametrize("quantize", [False, True])
+@pytest.mark.parametrize("mode", ["plain", "residual", "gate"])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows,D,groups", [(600, 10240, 16), (601, 8320, 16), (700, 12288, 16), (593, 12160, 16),
+                                           (600, 5120, 16), (600, 9600, 15), (600, 15360, 32)])
+def test_norm_many_rows_in_many_groups(ssd, rows, D, groups, dtype, mode, quantize):
+    """More than four rows to an SM, groups of 65 to 96 vectors of 16 bytes: the forms of
+    two and three vectors to a lane at their most warps."""
+    g = gen(rows + D)
+    kw = {}
+    if mode == "residual":
+        kw["residual"] = randn(g, rows, D, scale=2.0)
+    if mode == "gate":
+        kw["gate"] = randn(g, rows, D, dtype=dtype)
+    check_norm(ssd, randn(g, rows, D, dtype=dtype), 1 + 0.1 * randn(g, D), groups=groups, quantize=quantize, **kw)
