@@ -251,7 +251,10 @@ ssd_status ssd_rms_norm(const void* x, const void* residual, const void* gate, i
  *             base: those go to the tensor cores as they lie. Others are copied
  *             there first (fp32 as three bf16 parts, which keeps its 24 bits)
  *             unless reading a few tokens' worth as it lies takes less. It needs
- *             no clearing; calls ordered on one stream may share it.
+ *             no clearing; calls ordered on one stream may share it. fp32 operands
+ *             with a value that three bf16 parts do not add up to (infinities, NaN,
+ *             beyond bf16's largest, or below 2^-109 with bits below 2^-133) are
+ *             multiplied by fp32 FMAs instead, 3 to 12 times slower.
  *   Sizes: M, N >= 0 (0 is a no-op), K >= 1; M <= 2^30; N, K <= 2^20. x needs its
  *   element's alignment only; every other pointer is 16-byte aligned.
  *   The result does not depend on the path beyond rounding: bf16 products are

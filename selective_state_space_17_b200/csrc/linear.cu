@@ -978,8 +978,9 @@ cudaError_t run_out(const Operands& o, const Epilogue& e, bool out_bf16, const L
 //     x w = x1 w1 + (x1 w2 + x2 w1) + (x1 w3 + x2 w2 + x3 w1) + O(2^-24),
 // one product over six sections of K (and 6 of 1660 bf16 TFLOP/s against the
 // SIMT kernel's 37). Products of infinities do not split: when a value of the
-// operands does not fit bf16's range, the tensor-core kernel stands back and the
-// SIMT kernel computes the call.
+// operands does not fit bf16's range, at its top or with its last bits at its bottom,
+// the tensor-core kernel stands back and the SIMT kernel computes the call (64 x 10576 x
+// 2560 393 us instead of 114, 16384 x 10576 x 2560 43 ms instead of 3.7).
 cudaError_t linear_split(const LinearArgs& a, const Epilogue& e, char* ws, const LaunchCtx& ctx)
 {
     const Copies c = copies_of(a, Path::split);

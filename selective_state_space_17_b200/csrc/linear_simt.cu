@@ -192,8 +192,9 @@ __global__ void __launch_bounds__(kPackThreads) pack_rows_kernel(const T* src, l
 }
 
 // fp32 as the sum of three bf16, 24 significant bits in all: each is what the
-// ones before it leave, rounded, and the differences are exact. What bf16 cannot
-// hold (infinities, NaN, values that round to infinity) sets the flag.
+// ones before it leave, rounded, and the differences are exact. Where the parts are
+// not the value the flag is set: infinities, NaN, values that round to infinity, and
+// those below 2^-109 whose last bits lie below bf16's smallest value, 2^-133.
 __global__ void __launch_bounds__(kPackThreads) split_rows_kernel(const float* src, long long stride, int K,
                                                                   __nv_bfloat16* dst, int section, unsigned int* flag)
 {
@@ -206,7 +207,6 @@ __global__ void __launch_bounds__(kPackThreads) split_rows_kernel(const float* s
     for (int i = 0; i < kPackEach; ++i) {
         const int k = k0 + i * kPackThreads;
         v[i] = k < K ? s[k] : 0.0f;
-        odd |= !(fabsf(v[i]) <= 3.38953139e38f);  // the largest bf16
     }
 #pragma unroll
     for (int i = 0; i < kPackEach; ++i) {
@@ -215,9 +215,12 @@ __global__ void __launch_bounds__(kPackThreads) split_rows_kernel(const float* s
         const __nv_bfloat16 b1 = __float2bfloat16_rn(v[i]);
         const float r1 = v[i] - __bfloat162float(b1);
         const __nv_bfloat16 b2 = __float2bfloat16_rn(r1);
+        const float r2 = r1 - __bfloat162float(b2);
+        const __nv_bfloat16 b3 = __float2bfloat16_rn(r2);
         d[k] = b1;
         d[section + k] = b2;
-        d[2 * section + k] = __float2bfloat16_rn(r1 - __bfloat162float(b2));
+        d[2 * section + k] = b3;
+        odd |= !(__bfloat162float(b3) == r2);  // also where r2 is NaN: inf - inf
     }
     if (odd) *flag = 1u;  // every writer writes the same
 }

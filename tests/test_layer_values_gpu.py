@@ -78,3 +78,24 @@ def test_norm_many_rows_in_many_groups(ssd, rows, D, groups, dtype, mode, quanti
     if mode == "gate":
         kw["gate"] = randn(g, rows, D, dtype=dtype)
     check_norm(ssd, randn(g, rows, D, dtype=dtype), 1 + 0.1 * randn(g, D), groups=groups, quantize=quantize, **kw)
+
+
+# ------------------------------------------------------- products in fp32
+
+@pytest.mark.parametrize("M", [3, 70, 1100])
+@pytest.mark.parametrize("sx,sw", [(2.0 ** -124, 2.0 ** 110), (2.0 ** -112, 1.0), (2.0 ** 110, 2.0 ** -124),
+                                   (2.0 ** -140, 2.0 ** 120), (2.0 ** -105, 2.0 ** 90)])
+def test_linear_fp32_of_tiny_operands(ssd, M, sx, sw):
+    """Values whose third or second bf16 part would lie below bf16's range keep their 24
+    bits all the same; one such value among ordinary ones likewise."""
+    g = gen(M)
+    K = 96
+    x, w = randn(g, M, K) * sx, randn(g, 72, K) * sw
+    size = x.double().abs() @ w.double().abs().t()
+    check("y", ssd.linear(x, w), x.double() @ w.double().t(), size * (2 * K + 28) * U + K * DENORMAL)
+    x, w = randn(g, M, K), randn(g, 72, K)
+    x[M - 1] = 0
+    x[M - 1, 5] = sx * 1.2345678
+    w[:, 5] *= sw
+    size = x.double().abs() @ w.double().abs().t()
+    check("y", ssd.linear(x, w), x.double() @ w.double().t(), size * (2 * K + 28) * U + K * DENORMAL)
