@@ -316,7 +316,7 @@ linear_few_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
             }
             if (e.act != SSD_ACT_NONE) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[i][j] = activate(v[i][j], e.act);
+                for (int j = 0; j < 4; ++j) v[i][j] = activate<O>(v[i][j], e.act);
             }
             if (res) {
 #pragma unroll
@@ -463,7 +463,7 @@ __device__ __forceinline__ void store_row(const Epilogue& e, const void* residua
         for (int c = 0; c < CH; c += 8) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float t = gelu_f(v[j]);
+                const float t = gelu_f<O>(v[j]);
 #pragma unroll
                 for (int i = j; i + 8 < CH; i += 8) v[i] = v[i + 8];
                 v[CH - 8 + j] = t;
@@ -524,7 +524,7 @@ __device__ __forceinline__ void store_staged(const Epilogue& e, const void* resi
         }
         if (e.act != SSD_ACT_NONE) {
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) f[i] = activate(f[i], e.act);
+            for (int i = 0; i < kBatch; ++i) f[i] = activate<O>(f[i], e.act);
         }
         if (res) {
 #pragma unroll

@@ -26,7 +26,7 @@ __device__ __forceinline__ void finish(const LinearArgs& a, int m, int n, float 
     const long long at = (long long)m * a.N + n;
     if (a.x_scale) v = v * a.x_scale[m] * a.w_scale[n];
     if (a.bias) v += a.bias[n];
-    v = activate(v, a.act);
+    v = activate<O>(v, a.act);
     // residual may be y itself: a plain load
     if (a.residual) v += static_cast<float>(static_cast<const O*>(a.residual)[at]);
     io<O>::store(static_cast<O*>(a.y) + at, v);

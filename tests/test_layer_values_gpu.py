@@ -80,6 +80,39 @@ def test_norm_many_rows_in_many_groups(ssd, rows, D, groups, dtype, mode, quanti
     check_norm(ssd, randn(g, rows, D, dtype=dtype), 1 + 0.1 * randn(g, D), groups=groups, quantize=quantize, **kw)
 
 
+# -------------------------------------------------------------- activations
+
+def activated(ssd, v, act, out, M, variant=0):
+    """act(v) for v [N] by way of a product of zeros and the bias, on M equal rows."""
+    x = torch.zeros(M, 64, device="cuda", dtype=BF16)
+    w = torch.zeros(v.numel(), 64, device="cuda", dtype=BF16)
+    ssd.layer.set_linear_variant(variant)
+    try:
+        return ssd.linear(x, w, bias=v, activation=act, out_dtype=out)
+    finally:
+        ssd.layer.set_linear_variant(0)
+
+
+def gelu64(v):
+    return 0.5 * v * torch.special.erfc(-v / math.sqrt(2.0))
+
+
+@pytest.mark.parametrize("out", [F32, BF16])
+@pytest.mark.parametrize("M,variant", [(3, 1), (3, 2), (300, 2), (300, 3)])
+def test_linear_gelu_keeps_its_relative_precision(ssd, M, variant, out):
+    """The tail of v < 0, where the result is far below v: relative to the result. The
+    polynomial 4 U, its argument 2 U at a slope of 2.7, the power of two 5 U, products and
+    sums 6 U: 24 U in all. bf16 leaves out what fp32 makes up for: the exponent v^2 / 2 has
+    its square's, its factor's and their product's roundings, 1.25 v^2 U. erfc(-v) may lie
+    below fp32's normal range, each of two roundings within half a step."""
+    v = torch.cat([torch.linspace(-13, 10, 4093, device="cuda"), torch.tensor([0.0, 30.0, 1e30], device="cuda")])
+    got = activated(ssd, v, "gelu", out, M, variant)
+    want = gelu64(v.double())
+    rel = 24 * U + (1.25 * U * v.double().clamp(-20, 20) ** 2 + HALF[BF16] * 1.01 if out is BF16 else 0)
+    tol = want.abs() * rel + v.double().abs() * DENORMAL * (v < 0) + DENORMAL
+    check("gelu", got, want.expand(M, -1), tol.expand(M, -1))
+
+
 # ------------------------------------------------------- products in fp32
 
 @pytest.mark.parametrize("M", [3, 70, 1100])
