@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && VEC > 1 && kAhead 
                 float2 s = bias.pair(j);
 #pragma unroll
                 for (int k = 0; k < W; ++k) s = fma2(wt[k][j], win[k][j], s);
-                if (a.silu) s = silu2(s);
+                if (a.silu) s = silu2<T>(s);
                 v[2 * j] = s.x; v[2 * j + 1] = s.y;
 #pragma unroll
                 for (int k = 0; k < W - 1; ++k) win[k][j] = win[k + 1][j];

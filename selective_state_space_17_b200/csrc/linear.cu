@@ -455,7 +455,7 @@ __device__ __forceinline__ void store_row(const Epilogue& e, const void* residua
     }
     if (e.act == SSD_ACT_SILU) {
 #pragma unroll
-        for (int j = 0; j < CH; ++j) v[j] = silu_f(v[j]);
+        for (int j = 0; j < CH; ++j) v[j] = silu_f<O>(v[j]);
     } else if (e.act == SSD_ACT_GELU) {
         // rolled for the sake of the code's length; rotating the values by 8 keeps
         // their indexes constants

@@ -205,10 +205,10 @@ struct Operands {
         float2 v = x.pair(i);
         if constexpr (VEC == 1) {  // a single value beside a zero
             if constexpr (MODE == kResidual) v.x += r.get(0);
-            if constexpr (MODE == kGate) v.x *= silu_f(z.get(0));
+            if constexpr (MODE == kGate) v.x *= silu_f<T>(z.get(0));
         } else {
             if constexpr (MODE == kResidual) v = add2(v, r.pair(i));
-            if constexpr (MODE == kGate) v = mul2(v, silu2(z.pair(i)));
+            if constexpr (MODE == kGate) v = mul2(v, silu2<T>(z.pair(i)));
         }
         return v;
     }

@@ -97,6 +97,15 @@ def gelu64(v):
     return 0.5 * v * torch.special.erfc(-v / math.sqrt(2.0))
 
 
+def silu64(v):
+    return v / (1 + torch.exp(-v))
+
+
+# SiLU in fp32: e^-|v| (two units of 2^-23) times v, one plus it and the reciprocal (1 + 2),
+# the product: 10 U
+SILU_F32 = 10 * U
+
+
 @pytest.mark.parametrize("out", [F32, BF16])
 @pytest.mark.parametrize("M,variant", [(3, 1), (3, 2), (300, 2), (300, 3)])
 def test_linear_gelu_keeps_its_relative_precision(ssd, M, variant, out):
@@ -111,6 +120,43 @@ def test_linear_gelu_keeps_its_relative_precision(ssd, M, variant, out):
     rel = 24 * U + (1.25 * U * v.double().clamp(-20, 20) ** 2 + HALF[BF16] * 1.01 if out is BF16 else 0)
     tol = want.abs() * rel + v.double().abs() * DENORMAL * (v < 0) + DENORMAL
     check("gelu", got, want.expand(M, -1), tol.expand(M, -1))
+
+
+@pytest.mark.parametrize("M,variant", [(3, 1), (3, 2), (300, 2), (300, 3)])
+def test_linear_silu_keeps_its_relative_precision_in_fp32(ssd, M, variant):
+    """Down to where e^v leaves fp32's normal range, in which its two units are absolute."""
+    v = torch.cat([torch.linspace(-95, 30, 4093, device="cuda"), torch.tensor([0.0, 100.0, 1e30], device="cuda")])
+    got = activated(ssd, v, "silu", F32, M, variant)
+    want = silu64(v.double())
+    check("silu", got, want.expand(M, -1), (want.abs() * SILU_F32 + v.double().abs() * 4 * DENORMAL * (v < 0)).expand(M, -1))
+
+
+@pytest.mark.parametrize("width,H,P", [(4, 16, 64), (3, 15, 33), (2, 16, 64)])
+def test_conv_silu_keeps_its_relative_precision_in_fp32(ssd, width, H, P):
+    """Inputs of zero and the bias: act(v) of given values, in prompts and single tokens."""
+    G, N = 1, 20
+    C = H * P + 2 * G * N
+    v = torch.linspace(-95, 30, C, device="cuda")
+    u, w = torch.zeros(2, 11, C, device="cuda"), torch.ones(C, width, device="cuda")
+    want = silu64(v.double())
+    tol = want.abs() * SILU_F32 + v.double().abs() * 4 * DENORMAL * (v < 0)
+    x, Bm, Cm, _, _ = ssd.conv(u, w, v, H, P, G, N)
+    got = torch.cat([t.reshape(2, 11, -1) for t in (x, Bm, Cm)], -1)
+    check("conv", got, want.expand(2, 11, -1), tol.expand(2, 11, -1))
+    x, Bm, Cm, _ = ssd.conv_step(u[:, 0], w, v, torch.zeros(2, width - 1, C, device="cuda"), H, P, G, N)
+    got = torch.cat([t.reshape(2, -1) for t in (x, Bm, Cm)], -1)
+    check("conv_step", got, want.expand(2, -1), tol.expand(2, -1))
+
+
+@pytest.mark.parametrize("D", [64, 97, 2560, 20001])
+def test_norm_gate_keeps_its_relative_precision_in_fp32(ssd, D):
+    """Gates far below zero, whose squares are nothing beside eps = 1: y = silu(z) but for
+    the root's four units and three products'."""
+    z = torch.linspace(-80, -20, 5 * D, device="cuda").reshape(5, D)
+    one = torch.ones(5, D, device="cuda")
+    y, _, _ = ssd.rms_norm(one, one[0].clone(), gate=z, eps=1.0)
+    want = silu64(z.double())
+    check("y", y, want, want.abs() * (SILU_F32 + 8 * U))
 
 
 # ------------------------------------------------------- products in fp32
