@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && VEC > 1 && kAhead 
             for (int i = 0; i < kBatch; ++i) {
                 if (ts[i] >= t1) break;
                 float v = static_cast<float>(in[i]);
-                if (a.dt_bias) v += __ldg(a.dt_bias + hs[i]);
+                if (a.dt_bias) v += a.dt_bias[hs[i]];
                 a.dt[((long long)b * a.L + ts[i]) * a.H + hs[i]] = softplus_f(v);
             }
         }

@@ -98,6 +98,9 @@ inline bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintp
 // Programmatic dependent launch: a kernel launched by launch_overlapped may begin
 // while the one before it on the stream ends. Every thread waits here for that
 // one (all of it, and its writes) before it touches global memory.
+// Such a kernel reads with plain loads: the one before may have written any operand (the
+// norm the product's row scales), and a load by way of the read-only cache is for memory
+// that no one writes while the kernel runs, from before this wait on.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // From here on the next kernel's CTAs may take the room this kernel leaves, once

@@ -258,8 +258,8 @@ linear_few_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int nj = min(n + j * step, e.N - 1);
-        ws[j] = E4M3 ? __ldg(e.w_scale + nj) : 1.0f;
-        bias[j] = e.bias ? __ldg(e.bias + nj) : 0.0f;
+        ws[j] = E4M3 ? e.w_scale[nj] : 1.0f;
+        bias[j] = e.bias ? e.bias[nj] : 0.0f;
     }
     if (splits > 1) cluster_sync();
     else __syncthreads();
@@ -279,7 +279,7 @@ linear_few_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
 #pragma unroll
         for (int i = 0; i < TOKENS; ++i) {
             const int t = min(t0 + i * stride, tokens - 1);  // past the last: that one again
-            sx[i] = E4M3 ? __ldg(e.x_scale + m0 + t) : 1.0f;
+            sx[i] = E4M3 ? e.x_scale[m0 + t] : 1.0f;
             if (res) {
                 const O* from = res + (long long)(m0 + t) * e.N + n;
                 Packed<O, 4> r;
@@ -419,9 +419,9 @@ __device__ __forceinline__ void ld32(const void* p, uint32_t* w)
 }
 
 // Four consecutive fp32 values that start on 16 bytes.
-__device__ __forceinline__ void ldg4(const float* p, float* v)
+__device__ __forceinline__ void ld4(const float* p, float* v)
 {
-    const float4 f = __ldg(reinterpret_cast<const float4*>(p));
+    const float4 f = *reinterpret_cast<const float4*>(p);
     v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
 }
 
@@ -443,12 +443,12 @@ __device__ __forceinline__ void store_row(const Epilogue& e, const void* residua
     for (int c = 0; c < CH; c += 4) {
         float b[4];
         if constexpr (E4M3) {
-            ldg4(e.w_scale + n + c, b);
+            ld4(e.w_scale + n + c, b);
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[c + j] = v[c + j] * sx * b[j];
         }
         if (e.bias) {
-            ldg4(e.bias + n + c, b);
+            ld4(e.bias + n + c, b);
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[c + j] += b[j];
         }
@@ -499,8 +499,8 @@ __device__ __forceinline__ void store_staged(const Epilogue& e, const void* resi
     for (int j = 0; j < CH; ++j) turn[lane * (CH + 1) + j] = v[j];
     __syncwarp();
     const int c = lane % CH, nc = n + c;
-    const float ws = E4M3 ? __ldg(e.w_scale + min(nc, e.N - 1)) : 1.0f;
-    const float bias = e.bias ? __ldg(e.bias + min(nc, e.N - 1)) : 0.0f;
+    const float ws = E4M3 ? e.w_scale[min(nc, e.N - 1)] : 1.0f;
+    const float bias = e.bias ? e.bias[min(nc, e.N - 1)] : 0.0f;
     constexpr int kBatch = 8 < CH ? 8 : CH;  // rows under way together
     const int first = lane / CH;
     const int rows = nc < e.N ? min(32, e.M - m0) : 0;  // those of this lane's channel
@@ -683,7 +683,7 @@ linear_many_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             tile_at(tiles, i, im, in);
             const int m = im * 256 + (int)rank * 128 + quad * 32 + lane;
             const int n = in * BN + part * kCols;
-            const float sx = E4M3 && m < e.M ? __ldg(e.x_scale + m) : 1.0f;
+            const float sx = E4M3 && m < e.M ? e.x_scale[m] : 1.0f;
             float sum[SEG ? kCols : 1];
             // without an activation the sum may begin with the residual, which is
             // then read while the first products are under way

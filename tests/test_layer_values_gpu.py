@@ -178,3 +178,34 @@ def test_linear_fp32_of_tiny_operands(ssd, M, sx, sw):
     w[:, 5] *= sw
     size = x.double().abs() @ w.double().abs().t()
     check("y", ssd.linear(x, w), x.double() @ w.double().t(), size * (2 * K + 28) * U + K * DENORMAL)
+
+
+# ---------------------------------------------- kernels one after another
+
+def test_row_scales_of_the_kernel_before(ssd):
+    """A norm writes the scales that the product behind it reads, which starts while the
+    norm still runs: replays on changing rows give the bits of calls made one at a time."""
+    g = gen(4)
+    for M, D, N in ((1, 2048, 1024), (64, 2560, 1040), (700, 512, 2560)):
+        xs = [randn(g, M, D, dtype=BF16, scale=10.0 ** i) for i in range(-3, 4)]
+        weight = 1 + 0.1 * randn(g, D)
+        w, ws = quantize_rows(randn(g, N, D))
+        x, q, s = xs[0].clone(), torch.empty(M, D, device="cuda", dtype=E4M3), torch.empty(M, device="cuda")
+        y = torch.empty(M, N, device="cuda")
+        want = []
+        for v in xs:
+            x.copy_(v)
+            ssd.rms_norm(x, weight, eps=1.0, quantize=True, y=q, scale=s)
+            torch.cuda.synchronize()
+            want.append(ssd.linear(q, w, x_scale=s, w_scale=ws, out_dtype=F32))
+            torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(3):  # the product before still reads what the norm writes again
+                ssd.rms_norm(x, weight, eps=1.0, quantize=True, y=q, scale=s)
+                ssd.linear(q, w, x_scale=s, w_scale=ws, y=y)
+        for _ in range(5):
+            for v, expect in zip(xs, want):
+                x.copy_(v)
+                graph.replay()
+                assert torch.equal(y, expect), (M, D, N)
