@@ -202,7 +202,9 @@ ssd_status ssd_step(const void* x, const float* dt, const float* A, const void* 
  * a short convolution, the SSD core, gate and norm, the out-projection). They
  * follow the conventions at the top; strides count elements, and a strided
  * operand's last dimension is contiguous. Outputs must not overlap inputs or
- * each other except where an entry says so. Sums and statistics are fp32;
+ * each other except where an entry says so, which is judged by their spans from
+ * the first byte to the last (an output in the gap between two rows of a strided
+ * input is refused too). Sums and statistics are fp32;
  * an output is rounded once, to nearest even. Calls on different streams may
  * overlap freely, each with its own workspace where one is needed.
  */
@@ -225,8 +227,9 @@ ssd_status ssd_step(const void* x, const float* dt, const float* A, const void* 
  *   residual_out [rows, D] `residual_dtype`: v rounded (the norm itself reads
  *             v before this rounding); NULL to skip. May be residual itself.
  *   y may be x itself when y_dtype == dtype.
- *   A row that holds a NaN, or whose sum of squares overflows fp32, has NaN
- *   or zero outputs as the formulas in fp32 give them.
+ *   A row that holds a NaN, or whose sum of squares overflows fp32 (or with
+ *   eps = 0 falls below its normal range, values under 2^-63), has the NaN,
+ *   zero, infinite or coarse outputs that the formulas in fp32 give.
  *   Sizes: rows >= 0 (0 is a no-op), D in [1, 2^20], groups in [1, 32]
  *   dividing D.
  */
@@ -259,7 +262,7 @@ ssd_status ssd_rms_norm(const void* x, const void* residual, const void* gate, i
  *   element's alignment only; every other pointer is 16-byte aligned.
  *   The result does not depend on the path beyond rounding: bf16 products are
  *   exact in fp32 and added up there, where the tensor cores truncate; sums that
- *   reach an fp32 output are joined, rounded, about every 512 products.
+ *   reach an fp32 output are joined, rounded, every 768 products.
  */
 size_t ssd_linear_workspace_size(const void* x, int64_t x_stride, int M, int N, int K,
                                  ssd_dtype dtype);
@@ -333,9 +336,11 @@ int ssd_forward_path(int B, int L, int H, int P, int G, int N, int chunk, ssd_dt
  * SSD_ERR_CUDA (a CUDA error was pending on the stream). */
 ssd_status ssd_poll_status(ssd_stream_t stream);
 
-/* Test hook: sets the iteration limit of every device-side wait (0 restores
- * the default). A limit of 1 makes a wait that is not already satisfied give
- * up at once, which exercises the timeout path without hanging anything. */
+/* Test hook: sets the iteration limit of the waits for other CTAs' words in
+ * global memory (ssd_forward's look-back; 0 restores the default). A limit of 1
+ * makes such a wait that is not already satisfied give up at once, which exercises
+ * the timeout path without hanging anything. Waits on barriers in shared memory, all
+ * that ssd_linear has, keep their own limits of about 2 to 4 seconds. */
 void ssd_set_wait_limit(uint64_t iterations);
 
 /* Test hook: when `skip_publish` is nonzero, forward calls on the tensor-core

@@ -208,7 +208,8 @@ __device__ __forceinline__ float2 silu2(float2 v)
 // squares for the smallest largest relative error over 0 <= x <= 9.5: eight of them, 1.7e-7,
 // for bf16 (measured 2e-7 rms for v > -3.5, 1e-6 for v > -8; its rounding is 2e-3), ten,
 // 2.3e-9, for fp32, where t takes one Newton step and the rounding of the power's exponent is
-// made up for.
+// made up for (measured 1.1e-7 rms at most over -12 to 4, 4096 x 2560 x 512 29.3 us; erfcf
+// 0.7e-7 to 31e-7 and 39 us).
 template <typename O>
 __device__ __forceinline__ float gelu_f(float v)
 {

@@ -65,9 +65,10 @@ struct Epilogue {
 // ------------------------------------------------------------- few tokens
 
 // The tensor cores truncate each addition to an accumulator, a bias that grows with
-// the additions in a row: -4.7e-6 of the result after 5120 bf16 products, -0.8e-6
-// after 1024. fp32 outputs of bf16 operands are therefore summed in segments of
-// kSegBlocks blocks of K (768 products), joined in registers with rounded additions.
+// the additions in a row: after 5120 bf16 products -4.8e-6 of the result of normal
+// operands and -1.8e-5 of positive ones, after 1024 -0.9e-6 and -1.7e-6. fp32 outputs
+// of bf16 operands are therefore summed in segments of kSegBlocks blocks of K (768
+// products), joined in registers with rounded additions: -0.6e-6 and -1.3e-6 at any K.
 // A bf16 output's own rounding hides the bias, and products of e4m3 values, with
 // eight significant bits at most, lose next to nothing (1e-8 at K = 5120).
 constexpr int kSegBlocks = 12;
@@ -976,8 +977,8 @@ cudaError_t run_out(const Operands& o, const Epilogue& e, bool out_bf16, const L
 // fp32 operands on the bf16 tensor cores: x = x1 + x2 + x3 and w = w1 + w2 + w3
 // with 8 significant bits each, so
 //     x w = x1 w1 + (x1 w2 + x2 w1) + (x1 w3 + x2 w2 + x3 w1) + O(2^-24),
-// one product over six sections of K (and 6 of 1660 bf16 TFLOP/s against the
-// SIMT kernel's 37). Products of infinities do not split: when a value of the
+// one product over six sections of K (a sixth of the tensor cores' bf16 rate against the
+// SIMT kernel's 19 TFLOP/s). Products of infinities do not split: when a value of the
 // operands does not fit bf16's range, at its top or with its last bits at its bottom,
 // the tensor-core kernel stands back and the SIMT kernel computes the call (64 x 10576 x
 // 2560 393 us instead of 114, 16384 x 10576 x 2560 43 ms instead of 3.7).

@@ -197,7 +197,9 @@ def linear(x, w, bias=None, activation: str = "none", residual=None, x_scale=Non
     x may be a view with evenly spaced rows. bias [N] is fp32; activation is
     "none", "silu" or "gelu" (the one with erf); residual has the output's dtype
     and shape and may be y. The output [..., N] is out_dtype, by default y's, the
-    residual's or x's dtype, and bf16 for 8-bit operands."""
+    residual's or x's dtype, and bf16 for 8-bit operands. fp32 operands keep their 24
+    bits; infinities, NaN and values at the ends of the range (include/ssd.h) make the
+    call several times slower."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         _need(x, "x")
     code = _OPERAND.get(x.dtype)

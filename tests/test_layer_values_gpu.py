@@ -203,9 +203,9 @@ def test_linear_fp32_of_tiny_operands(ssd, M, sx, sw):
 @pytest.mark.parametrize("variant,M,N", [(2, 64, 20480), (3, 512, 2560)])
 def test_linear_long_sums_are_not_biased(ssd, variant, M, N):
     """The tensor cores truncate as they add: a sum of 5120 positive products in one
-    accumulator comes out 4.7e-6 too small on average. Joined every 768 products, 48
-    additions of 16, it loses half a step of 2^-23 an addition of a sum that grows evenly:
-    24 x 2^-24 on average."""
+    accumulator comes out 1.8e-5 too small on average. Joined every 768 products, 48
+    additions of 16, it loses half a step of at most 2^-23 an addition of a sum that grows
+    evenly: 24 x 2^-24 = 1.43e-6."""
     g = gen(variant)
     K = 5120
     x = torch.rand(M, K, generator=g, device="cuda").to(BF16)
